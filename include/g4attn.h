@@ -349,6 +349,113 @@ g4_status g4attn_decode_static(const g4attn_layer* layer, const void* q, const v
                                const g4attn_cache* cache, const int32_t* page_table,
                                int32_t max_pages, void* out, void* stream);
 
+/* ---- The 8-bit paged cache ---------------------------------------------------------------------
+ * A cache of half the bytes: keys and values as 8-bit codes with one power-of-two step per token and
+ * head. The RFC this library follows has no counterpart of it (its cache is bf16); it exists for
+ * serving processes whose contexts outgrow the device memory.
+ *
+ * Values. A head vector x, normed and turned in fp32 (sliding: K' and V; global: S, and p-RoPE(K) on
+ * the 128 turned columns d in [0, 64) U [256, 320)), is stored as
+ *   a = max |x|,  E = floor(log2 a) - 6,  code = clamp(round_half_even(x / 2^E), -127, 127),
+ * one byte code + 128 per column and one exponent byte E + 133 per vector. When a < 2^-119 the
+ * exponent byte is 0 and all codes are 0; when x holds an infinity or NaN it is 255 and the whole
+ * vector reads as NaN, so that a bad vector shows in every row that sees it. The value, code * 2^E, is
+ * a bf16 number. The step belongs to one token and one head: a key's bytes never depend on the
+ * batch, on the chunks its prompt came in, or on later tokens, so the calls below are batch-invariant
+ * like the bf16 ones.
+ *
+ * Layout. pages holds one block per (page, KV head), 16 keys each, blocks of
+ *   sliding 8224 bytes: [K' tile, 4096][V tile, 4096][16 exponents of K'][16 of V],
+ *   global 10272 bytes: [S tile, 8192][turned columns, 2048][16 exponents of S][16 of the turned],
+ * at pages + (page * n_kv_heads + head) * block. A tile is [columns / 128][16 keys][128 bytes]; the
+ * 16-byte piece c of key j's 128 bytes sits at piece c ^ (j & 6) ^ 4 (j & 1). The turned columns are in
+ * the order [0, 64) then [256, 320). pages is 16-byte aligned. Slots that no key was written to may hold
+ * anything. */
+typedef struct {
+  void* pages;
+  int32_t num_pages;      /* physical pages */
+  int32_t page_size;      /* keys per page; must be 16 */
+} g4attn_cache8;
+
+/* Bytes of one page (all KV heads) of the layer's 8-bit cache; 0 for an unsupported layer. The RFC has
+ * no counterpart. */
+size_t g4attn_kv8_page_bytes(const g4attn_layer* layer);
+
+/* g4attn_kv_append_normed into an 8-bit cache (the RFC has no counterpart of it): writes the
+ * rows' K' and V, or S and its turned columns. Row conventions and errors as there; norms may be NULL.
+ * A sequence whose rows do not lie inside [0, T), or whose positions do not lie inside [0, 262144), is
+ * refused on the device (G4_ERR_DEVICE), and so is each row whose page is not in the table or the pool. */
+g4_status g4attn_kv8_append(const g4attn_layer* layer, const g4attn_norms* norms, const void* k, const void* v,
+                            int32_t T, const int32_t* q_start, const int32_t* q_len, const int32_t* ctx_start,
+                            int32_t B, const g4attn_cache8* cache, const int32_t* page_table, int32_t max_pages,
+                            void* stream);
+
+/* Reads keys back (no counterpart in the RFC): keys key_begin[b] .. key_end[b]-1 (int32 [B], device;
+ * empty when key_end <= key_begin) of each sequence b go, as bf16, from the 8-bit pages of page_table
+ * into the pages of the same logical index of out_table, in the bf16 layout of g4attn_cache, for the
+ * calls that read that layout (g4attn_prefill_attend, g4attn_prefill_partial, g4attn_decode). Both tables
+ * have max_pages columns. Slots of other keys are not written. Logical pages that two sequences map to
+ * one destination page are written twice, in no order. Errors: a range outside [0, min(262144, 16 *
+ * max_pages)) is refused whole, a page outside either pool is skipped (G4_ERR_DEVICE). */
+g4_status g4attn_kv8_unpack(const g4attn_layer* layer, const int32_t* key_begin, const int32_t* key_end, int32_t B,
+                            const g4attn_cache8* cache, const int32_t* page_table, const g4attn_cache* out,
+                            const int32_t* out_table, int32_t max_pages, void* stream);
+
+/* Prefill, or one chunk of a chunked prefill, over an 8-bit cache (no counterpart in the RFC):
+ * g4attn_prefill_vision whose keys and values, the new rows' own among them, are the stored 8-bit
+ * values. The new rows are appended (as g4attn_kv8_append), the keys that some row sees (from
+ * ctx_start - window + 1 on sliding layers, from 0 on global ones, to ctx_start + q_len - 1) are read
+ * back into `scratch` (as g4attn_kv8_unpack; a caller's bf16 cache of that many pages, which layers and
+ * calls ordered on one stream can share), and the attention runs over them. On return scratch holds
+ * those keys' values (and zeros before the first of them in its page). norms and span may be NULL. A row's output does not depend on the batch around it
+ * or on the chunks. Other arguments and errors as g4attn_prefill_vision; scratch_table: int32
+ * [B][max_pages], the scratch page of each logical page a row of sequence b sees, distinct between
+ * sequences. */
+g4_status g4attn_kv8_prefill(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k,
+                             const void* v, int32_t T, const int32_t* q_start, const int32_t* q_len,
+                             const int32_t* ctx_start, int32_t B, const int32_t* span, const g4attn_cache8* cache,
+                             const int32_t* page_table, const g4attn_cache* scratch, const int32_t* scratch_table,
+                             int32_t max_pages, void* out, void* stream);
+
+/* Bytes of workspace g4attn_kv8_decode needs (no counterpart in the RFC); page_weights: 1 when that
+ * call gets page_weights (global layers). 0 for an unsupported layer, B <= 0 or max_pages <= 0. */
+size_t g4attn_kv8_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, int32_t max_pages,
+                                         int32_t page_weights);
+
+/* One decode step over an 8-bit cache (no counterpart in the RFC): g4attn_decode_normed, with the same
+ * fixed chunks and merge order, and three additions.
+ *   k_new, v_new   both may be NULL: the newest token is in the cache already (g4attn_kv8_append).
+ *   pos            int32 [B], device, or NULL: the RoPE position of each request's newest token. NULL:
+ *                  seq_len[b] - 1. A sequence that lost pages (g4attn_evict_pages) holds seq_len[b] keys,
+ *                  fewer than its positions: seq_len[b] - 1 <= pos[b] < 262144 (else G4_ERR_DEVICE, and a
+ *                  row of zeros). The mask goes by the held keys: all of them on global layers, the last
+ *                  `window` held ones on sliding layers.
+ *   page_weights   float [B][max_pages], device, or NULL; global layers only (G4_ERR_UNSUPPORTED else):
+ *                  page_weights[b][i] += the softmax weight of held page i's keys, summed over the
+ *                  query heads (a step adds n_q_heads over a sequence's pages). Entries past the held
+ *                  pages are not touched. Calls that share a buffer must be ordered.
+ * The query is turned and cast to bf16; the softmax weights are cast to fp16 for the value product. */
+g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k_new,
+                            const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B,
+                            const g4attn_cache8* cache, const int32_t* page_table, int32_t max_pages,
+                            float* page_weights, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Evicts whole pages from each sequence's page table by accumulated weight (no counterpart in the
+ * RFC). Sequence b holds n = ceil(seq_len[b] / 16) pages. When n > keep_pages, the n - keep_pages lightest
+ * of its evictable pages leave: all but the first first_pages and the last last_pages (first_pages >= 0,
+ * last_pages >= 1, first_pages + last_pages <= keep_pages). Of equal weights the lower index leaves
+ * first; a NaN counts as the heaviest. No key moves: the table is closed up, in order.
+ *   out_seq_len [B]             seq_len - 16 per evicted page
+ *   out_table, out_weights [B][max_pages]  the kept pages and their weights, then -1 and 0
+ *   freed [B][max_pages], n_freed [B]      the evicted physical pages in their order, then -1
+ * out_seq_len, out_table and out_weights may be the inputs. max_pages <= 16384. All arrays are device
+ * int32 (weights: float). A sequence whose seq_len is below 0, past 262144 or past the table is passed
+ * on whole (its max_pages entries) and sets G4_ERR_DEVICE. */
+g4_status g4attn_evict_pages(const int32_t* seq_len, const int32_t* page_table, const float* page_weights, int32_t B,
+                             int32_t max_pages, int32_t keep_pages, int32_t first_pages, int32_t last_pages,
+                             int32_t* out_seq_len, int32_t* out_table, float* out_weights, int32_t* freed,
+                             int32_t* n_freed, void* stream);
+
 /* Runtime provenance (RFC section 4, rule 8): writes a NUL-terminated one-line record
  * (backend, kernel ids, schedule, split policy, accumulator, layer kind, device, dtype,
  * fallback state) into buf. Returns the record's length without the NUL, or -1 when the

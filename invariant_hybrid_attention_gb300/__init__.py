@@ -27,7 +27,9 @@ EXPORTS = ("g4attn_rope_apply", "g4attn_prefill", "g4attn_prefill_stage", "g4att
            "g4attn_decode_exact", "g4attn_decode_exact_workspace_bytes",
            "g4attn_kv_append", "g4attn_decode_workspace_bytes",
            "g4attn_decode", "g4attn_decode_static", "g4attn_provenance", "g4attn_status_sync", "g4attn_status_string",
-           "g4attn_set_wait_limit_ns", "g4attn_wait_limit_ns", "g4attn_prefill_partial", "g4attn_merge_partials")
+           "g4attn_set_wait_limit_ns", "g4attn_wait_limit_ns", "g4attn_prefill_partial", "g4attn_merge_partials",
+           "g4attn_kv8_page_bytes", "g4attn_kv8_append", "g4attn_kv8_unpack", "g4attn_kv8_prefill",
+           "g4attn_kv8_decode_workspace_bytes", "g4attn_kv8_decode", "g4attn_evict_pages")
 DEFAULT_WAIT_LIMIT_NS = 2_000_000_000   # the kernels' bounded waits give up after 2 s by default
 
 
@@ -45,6 +47,10 @@ class g4attn_norms(ctypes.Structure):
 class g4attn_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_rot", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class g4attn_cache8(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
 
 class G4Error(RuntimeError):
@@ -67,7 +73,7 @@ def load(path: Optional[str] = None):
     lib = ctypes.CDLL(p)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     L, C = ctypes.POINTER(g4attn_layer), ctypes.POINTER(g4attn_cache)
-    N = ctypes.POINTER(g4attn_norms)
+    N, C8 = ctypes.POINTER(g4attn_norms), ctypes.POINTER(g4attn_cache8)
     sigs = {
         "g4attn_rope_apply": (I32, [L, P, P, I32, I32, P, P]),
         "g4attn_prefill": (I32, [L, P, P, P, I32, P, P, P, I32, C, P, I32, P, P]),
@@ -91,6 +97,13 @@ def load(path: Optional[str] = None):
         "g4attn_prefill_partial": (I32, [L, P, I32, P, P, P, I32, P, P, C, P, I32, P, P, P]),
         "g4attn_merge_partials": (I32, [L, I32, ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p),
                                         I32, P, P, I32, P, P]),
+        "g4attn_kv8_page_bytes": (SZ, [L]),
+        "g4attn_kv8_append": (I32, [L, N, P, P, I32, P, P, P, I32, C8, P, I32, P]),
+        "g4attn_kv8_unpack": (I32, [L, P, P, I32, C8, P, C, P, I32, P]),
+        "g4attn_kv8_prefill": (I32, [L, N, P, P, P, I32, P, P, P, I32, P, C8, P, C, P, I32, P, P]),
+        "g4attn_kv8_decode_workspace_bytes": (SZ, [L, I32, I32, I32]),
+        "g4attn_kv8_decode": (I32, [L, N, P, P, P, P, P, I32, C8, P, I32, P, P, P, SZ, P]),
+        "g4attn_evict_pages": (I32, [P, P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -321,3 +334,120 @@ def g4attn_merge_partials(layer, o_parts, ml_parts, q_start, q_len, out, stream=
     _check(load().g4attn_merge_partials(ctypes.byref(layer), n, arr_o, arr_m, T, _ptr(q_start), _ptr(q_len), B,
                                         _ptr(out), _stream(stream)), "g4attn_merge_partials")
     return out
+
+
+# ---- the 8-bit paged cache ----------------------------------------------------------------------------
+# The kernels take dense tensors of one type on the current device; these calls check that, since a
+# raw pointer cannot say otherwise.
+
+def make_cache8(pages, num_pages: int) -> g4attn_cache8:
+    return g4attn_cache8(_ptr(pages), int(num_pages), PAGE_SIZE)
+
+
+def _tensors(what: str, *specs):
+    """Checks (name, tensor or None, dtype, shape) of a call; None and raw addresses pass."""
+    import torch
+    here = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    elsewhere = None
+    for name, t, dtype, shape in specs:
+        if t is None or isinstance(t, int):
+            continue
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be a dense {dtype} tensor of shape {tuple(shape)}, got "
+                             f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (strided)'}")
+        if t.get_device() != here or here < 0:
+            elsewhere = elsewhere or (name, t.device)
+    if elsewhere:
+        raise ValueError(f"{what}: {elsewhere[0]} is on {elsewhere[1]}, not on the current CUDA device")
+
+
+def _opt(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def g4attn_kv8_page_bytes(layer) -> int:
+    return int(load().g4attn_kv8_page_bytes(ctypes.byref(layer)))
+
+
+def g4attn_kv8_append(layer, norms, k, v, q_start, q_len, ctx_start, cache: g4attn_cache8, page_table, stream=None):
+    """g4attn_kv_append_normed into an 8-bit cache; norms may be None."""
+    import torch
+    T, B, bf, i32 = k.shape[0], q_start.shape[0], torch.bfloat16, torch.int32
+    kv = (T, layer.n_kv_heads, layer.head_dim)
+    _tensors("g4attn_kv8_append", ("k", k, bf, kv), ("v", v, bf, kv), ("q_start", q_start, i32, (B,)),
+             ("q_len", q_len, i32, (B,)), ("ctx_start", ctx_start, i32, (B,)),
+             ("page_table", page_table, i32, (B, page_table.shape[-1])))
+    _check(load().g4attn_kv8_append(ctypes.byref(layer), _opt(norms), _ptr(k), _ptr(v), T, _ptr(q_start), _ptr(q_len),
+                                    _ptr(ctx_start), B, ctypes.byref(cache), _ptr(page_table), page_table.shape[1],
+                                    _stream(stream)), "g4attn_kv8_append")
+
+
+def g4attn_kv8_unpack(layer, key_begin, key_end, cache: g4attn_cache8, page_table, out: g4attn_cache, out_table,
+                      stream=None):
+    """Reads keys key_begin[b] .. key_end[b]-1 back as bf16 pages of `out` (through out_table)."""
+    import torch
+    B, i32 = key_begin.shape[0], torch.int32
+    table = (B, page_table.shape[-1])
+    _tensors("g4attn_kv8_unpack", ("key_begin", key_begin, i32, (B,)), ("key_end", key_end, i32, (B,)),
+             ("page_table", page_table, i32, table), ("out_table", out_table, i32, table))
+    _check(load().g4attn_kv8_unpack(ctypes.byref(layer), _ptr(key_begin), _ptr(key_end), B, ctypes.byref(cache),
+                                    _ptr(page_table), ctypes.byref(out), _ptr(out_table), table[1], _stream(stream)),
+           "g4attn_kv8_unpack")
+
+
+def g4attn_kv8_prefill(layer, norms, q, k, v, q_start, q_len, ctx_start, cache: g4attn_cache8, page_table,
+                       scratch: g4attn_cache, scratch_table, out, span=None, stream=None):
+    """A prefill (or chunk) over an 8-bit cache; scratch: a bf16 cache for the keys its rows see."""
+    import torch
+    T, B, bf, i32 = q.shape[0], q_start.shape[0], torch.bfloat16, torch.int32
+    qo, kv = (T, layer.n_q_heads, layer.head_dim), (T, layer.n_kv_heads, layer.head_dim)
+    table = (B, page_table.shape[-1])
+    _tensors("g4attn_kv8_prefill", ("q", q, bf, qo), ("k", k, bf, kv), ("v", v, bf, kv), ("out", out, bf, qo),
+             ("q_start", q_start, i32, (B,)), ("q_len", q_len, i32, (B,)), ("ctx_start", ctx_start, i32, (B,)),
+             ("page_table", page_table, i32, table), ("scratch_table", scratch_table, i32, table),
+             ("span", span, i32, (T, 2)))
+    _check(load().g4attn_kv8_prefill(ctypes.byref(layer), _opt(norms), _ptr(q), _ptr(k), _ptr(v), T, _ptr(q_start),
+                                     _ptr(q_len), _ptr(ctx_start), B, _ptr(span), ctypes.byref(cache),
+                                     _ptr(page_table), ctypes.byref(scratch), _ptr(scratch_table), table[1], _ptr(out),
+                                     _stream(stream)), "g4attn_kv8_prefill")
+    return out
+
+
+def g4attn_kv8_decode_workspace_bytes(layer, B: int, max_pages: int, page_weights: bool = False) -> int:
+    return int(load().g4attn_kv8_decode_workspace_bytes(ctypes.byref(layer), int(B), int(max_pages),
+                                                        1 if page_weights else 0))
+
+
+def g4attn_kv8_decode(layer, norms, q, k_new, v_new, seq_len, cache: g4attn_cache8, page_table, out, workspace,
+                      pos=None, page_weights=None, stream=None):
+    """One decode step over an 8-bit cache. k_new None: the newest token is in the cache already; pos:
+    RoPE positions of sequences that lost pages; page_weights: accumulated per page (global layers)."""
+    import torch
+    B, bf, i32 = q.shape[0], torch.bfloat16, torch.int32
+    qo, kv = (B, layer.n_q_heads, layer.head_dim), (B, layer.n_kv_heads, layer.head_dim)
+    table = (B, page_table.shape[-1])
+    _tensors("g4attn_kv8_decode", ("q", q, bf, qo), ("k_new", k_new, bf, kv), ("v_new", v_new, bf, kv),
+             ("out", out, bf, qo), ("seq_len", seq_len, i32, (B,)), ("pos", pos, i32, (B,)),
+             ("page_table", page_table, i32, table), ("page_weights", page_weights, torch.float32, table))
+    _check(load().g4attn_kv8_decode(ctypes.byref(layer), _opt(norms), _ptr(q), _ptr(k_new), _ptr(v_new),
+                                    _ptr(seq_len), _ptr(pos), B, ctypes.byref(cache), _ptr(page_table), table[1],
+                                    _ptr(page_weights), _ptr(out), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)),
+           "g4attn_kv8_decode")
+    return out
+
+
+def g4attn_evict_pages(seq_len, page_table, page_weights, keep_pages: int, first_pages: int, last_pages: int,
+                       out_seq_len, out_table, out_weights, freed, n_freed, stream=None):
+    """Evicts each sequence's lightest pages down to keep_pages; the out_ tensors may be the inputs."""
+    import torch
+    B, i32, f32 = seq_len.shape[0], torch.int32, torch.float32
+    table = (B, page_table.shape[-1])
+    _tensors("g4attn_evict_pages", ("seq_len", seq_len, i32, (B,)), ("page_table", page_table, i32, table),
+             ("page_weights", page_weights, f32, table), ("out_seq_len", out_seq_len, i32, (B,)),
+             ("out_table", out_table, i32, table), ("out_weights", out_weights, f32, table),
+             ("freed", freed, i32, table), ("n_freed", n_freed, i32, (B,)))
+    _check(load().g4attn_evict_pages(_ptr(seq_len), _ptr(page_table), _ptr(page_weights), B, table[1], int(keep_pages),
+                                     int(first_pages), int(last_pages), _ptr(out_seq_len), _ptr(out_table),
+                                     _ptr(out_weights), _ptr(freed), _ptr(n_freed), _stream(stream)),
+           "g4attn_evict_pages")

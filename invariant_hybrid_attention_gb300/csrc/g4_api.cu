@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "g4_internal.h"
+#include "g4_kv8.cuh"
 #include "g4attn.h"
 
 using namespace g4;
@@ -103,6 +104,17 @@ g4_status check_norms(const g4attn_norms* n, bool global, NormArgs* out) {
   out->v_norm = n->v_norm;
   out->eps = n->eps;
   return G4_OK;
+}
+
+g4_status check_cache8(const g4attn_cache8* c, const int32_t* page_table, int32_t max_pages) {
+  if (!c || !c->pages || !aligned16(c->pages)) return G4_ERR_INVALID;
+  if (c->page_size != kPage) return G4_ERR_UNSUPPORTED;
+  if (c->num_pages <= 0 || max_pages <= 0 || !page_table) return G4_ERR_INVALID;
+  return G4_OK;
+}
+
+PagedCache8 paged8(const g4attn_layer* L, const g4attn_cache8* c, const int32_t* page_table, int32_t max_pages) {
+  return PagedCache8{(uint8_t*)c->pages, c->num_pages, page_table, max_pages, L->n_q_heads, L->n_kv_heads};
 }
 
 // Scratch of g4attn_decode_static: the partial softmax states of one decode step, in a
@@ -429,6 +441,140 @@ g4_status g4attn_decode_static(const g4attn_layer* layer, const void* q, const v
   if (decode_scratch(&ws) != cudaSuccess) return G4_ERR_CUDA;
   return g4attn_decode(layer, q, k_new, v_new, seq_len, B, cache, page_table, max_pages, out, ws,
                        G4ATTN_DECODE_STATIC_SCRATCH_BYTES, stream);
+}
+
+size_t g4attn_kv8_page_bytes(const g4attn_layer* layer) {
+  bool global = false;
+  if (check_layer(layer, &global) != G4_OK) return 0;
+  return (size_t)layer->n_kv_heads * (global ? Kv8Block<true>::kBytes : Kv8Block<false>::kBytes);
+}
+
+g4_status g4attn_kv8_append(const g4attn_layer* layer, const g4attn_norms* norms, const void* k, const void* v,
+                            int32_t T, const int32_t* q_start, const int32_t* q_len, const int32_t* ctx_start,
+                            int32_t B, const g4attn_cache8* cache, const int32_t* page_table, int32_t max_pages,
+                            void* stream) {
+  bool global = false;
+  g4_status s = check_layer(layer, &global);
+  if (s != G4_OK) return s;
+  NormArgs nm;
+  if ((s = check_norms(norms, global, &nm)) != G4_OK) return s;
+  if ((s = check_rows(k, T, q_start, q_len, ctx_start, B)) != G4_OK) return s;
+  if ((s = check_cache8(cache, page_table, max_pages)) != G4_OK) return s;
+  if (global ? v != nullptr : (T > 0 && (!v || !aligned16(v)))) return G4_ERR_INVALID;
+  if (T == 0) return G4_OK;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  const SeqRows rows{q_start, q_len, ctx_start, B, T};
+  return from_cuda(launch_kv8_append(global, k, v, rows, paged8(layer, cache, page_table, max_pages), nm, st,
+                                     (cudaStream_t)stream));
+}
+
+g4_status g4attn_kv8_unpack(const g4attn_layer* layer, const int32_t* key_begin, const int32_t* key_end, int32_t B,
+                            const g4attn_cache8* cache, const int32_t* page_table, const g4attn_cache* out,
+                            const int32_t* out_table, int32_t max_pages, void* stream) {
+  bool global = false;
+  g4_status s = check_layer(layer, &global);
+  if (s != G4_OK) return s;
+  if (B <= 0 || !key_begin || !key_end) return G4_ERR_INVALID;
+  if ((s = check_cache8(cache, page_table, max_pages)) != G4_OK) return s;
+  if ((s = check_cache(out, global, out_table, max_pages)) != G4_OK) return s;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  const Kv8Range range{key_begin, key_end, SeqRows{nullptr, nullptr, nullptr, B, 0}, 0};
+  return from_cuda(launch_kv8_unpack(global, range, paged8(layer, cache, page_table, max_pages),
+                                     paged(layer, out, out_table, max_pages), st, (cudaStream_t)stream));
+}
+
+g4_status g4attn_kv8_prefill(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k,
+                             const void* v, int32_t T, const int32_t* q_start, const int32_t* q_len,
+                             const int32_t* ctx_start, int32_t B, const int32_t* span, const g4attn_cache8* cache,
+                             const int32_t* page_table, const g4attn_cache* scratch, const int32_t* scratch_table,
+                             int32_t max_pages, void* out, void* stream) {
+  bool global = false;
+  g4_status s = check_layer(layer, &global);
+  if (s != G4_OK) return s;
+  NormArgs nm;
+  if ((s = check_norms(norms, global, &nm)) != G4_OK) return s;
+  if ((s = check_rows(q, T, q_start, q_len, ctx_start, B)) != G4_OK) return s;
+  if ((s = check_cache8(cache, page_table, max_pages)) != G4_OK) return s;
+  if ((s = check_cache(scratch, global, scratch_table, max_pages)) != G4_OK) return s;
+  if (T > 0 && (!k || !aligned16(k) || !out || !aligned16(out))) return G4_ERR_INVALID;
+  if (global ? v != nullptr : (T > 0 && (!v || !aligned16(v)))) return G4_ERR_INVALID;
+  if (span && (reinterpret_cast<uintptr_t>(span) & 7u)) return G4_ERR_INVALID;
+  if (T == 0) return G4_OK;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  const cudaStream_t cs = (cudaStream_t)stream;
+  const SeqRows rows{q_start, q_len, ctx_start, B, T, span};
+  const PagedCache8 c8 = paged8(layer, cache, page_table, max_pages);
+  const PagedCache c16 = paged(layer, scratch, scratch_table, max_pages);
+  const int window = global ? 0 : layer->window;
+  if (launch_kv8_append(global, k, v, rows, c8, nm, st, cs) != cudaSuccess) return G4_ERR_CUDA;
+  const Kv8Range range{nullptr, nullptr, rows, window};
+  if (launch_kv8_unpack(global, range, c8, c16, st, cs) != cudaSuccess) return G4_ERR_CUDA;
+  // Plain queries are turned inside the attention kernel; normed ones, and those of a call with image
+  // spans, are staged in `out` first.
+  const bool staged = nm.any() || span != nullptr;
+  if (staged && launch_stage_queries(global, q, out, rows, c16, st, cs, nm) != cudaSuccess) return G4_ERR_CUDA;
+  return from_cuda(launch_prefill(global, rows, window, scale_log2(layer), c16, out, st, cs, staged ? nullptr : q));
+}
+
+size_t g4attn_kv8_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, int32_t max_pages,
+                                         int32_t page_weights) {
+  bool global = false;
+  if (check_layer(layer, &global) != G4_OK || B <= 0 || max_pages <= 0 || (page_weights && !global)) return 0;
+  return kv8_decode_workspace_bytes(global, B, max_pages, global ? 0 : layer->window, layer->n_q_heads,
+                                    layer->n_kv_heads, page_weights != 0);
+}
+
+g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k_new,
+                            const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B,
+                            const g4attn_cache8* cache, const int32_t* page_table, int32_t max_pages,
+                            float* page_weights, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  bool global = false;
+  g4_status s = check_layer(layer, &global);
+  if (s != G4_OK) return s;
+  NormArgs nm;
+  if ((s = check_norms(norms, global, &nm)) != G4_OK) return s;
+  if (page_weights && !global) return G4_ERR_UNSUPPORTED;
+  if (B <= 0 || !q || !seq_len || !out || !workspace) return G4_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return G4_ERR_INVALID;
+  if (k_new ? !aligned16(k_new) || (global ? v_new != nullptr : (!v_new || !aligned16(v_new))) : v_new != nullptr)
+    return G4_ERR_INVALID;
+  if ((s = check_cache8(cache, page_table, max_pages)) != G4_OK) return s;
+  const int window = global ? 0 : layer->window;
+  if (workspace_bytes < kv8_decode_workspace_bytes(global, B, max_pages, window, layer->n_q_heads, layer->n_kv_heads,
+                                                   page_weights != nullptr))
+    return G4_ERR_INVALID;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  const cudaStream_t cs = (cudaStream_t)stream;
+  const PagedCache8 c8 = paged8(layer, cache, page_table, max_pages);
+  const void* q_eff = q;   // normed queries go through `out`, as in g4attn_decode_normed
+  if (nm.wq != nullptr || (global && nm.wk != nullptr)) {
+    if (launch_norm_queries(global, q, out, B, layer->n_q_heads, nm, cs) != cudaSuccess) return G4_ERR_CUDA;
+    q_eff = out;
+  }
+  if (k_new && launch_kv8_append_decode(global, k_new, v_new, seq_len, pos, B, c8, nm, st, cs) != cudaSuccess)
+    return G4_ERR_CUDA;
+  return from_cuda(launch_kv8_decode(global, q_eff, seq_len, pos, B, window, scale_log2(layer), c8, page_weights, out,
+                                     workspace, st, cs));
+}
+
+g4_status g4attn_evict_pages(const int32_t* seq_len, const int32_t* page_table, const float* page_weights, int32_t B,
+                             int32_t max_pages, int32_t keep_pages, int32_t first_pages, int32_t last_pages,
+                             int32_t* out_seq_len, int32_t* out_table, float* out_weights, int32_t* freed,
+                             int32_t* n_freed, void* stream) {
+  if (B <= 0 || max_pages <= 0 || max_pages > kMaxPos / kPage) return G4_ERR_INVALID;
+  if (first_pages < 0 || last_pages < 1 || keep_pages < 1 || first_pages > keep_pages - last_pages)
+    return G4_ERR_INVALID;
+  if (!seq_len || !page_table || !page_weights || !out_seq_len || !out_table || !out_weights || !freed || !n_freed)
+    return G4_ERR_INVALID;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  return from_cuda(launch_evict_pages(seq_len, page_table, page_weights, B, max_pages, keep_pages, first_pages,
+                                      last_pages, out_seq_len, out_table, out_weights, freed, n_freed, st,
+                                      (cudaStream_t)stream));
 }
 
 int32_t g4attn_provenance(const g4attn_layer* layer, char* buf, size_t len) {

@@ -1,0 +1,574 @@
+// Decode over the 8-bit paged cache: one query token per request, its keys split into the fixed
+// chunks of the bf16 decode (256 keys on sliding layers, 1024 on global ones, aligned to key 0) and
+// merged in ascending chunk order; inside a chunk page i goes to warp i % 4 and the warps' states
+// merge in warp order. Every number a request gets depends on its own position, window and data.
+//
+// The stored bytes are codes u = 128 + c of values c 2^e with one exponent e per key and tile
+// (g4_kv8.cuh). The matrix instructions (m16n8k16, fp16 operands, fp32 sums) take the codes as they
+// are: 0x6400 | u is the fp16 number 1024 + u, and subtracting 1152 leaves c exactly. The powers of
+// two stay outside:
+//   scores   x_j = scale log2(e) 2^e_j (c_j . q), with q as fp16 scaled by a power of two per head
+//            (the bf16 q' is exact there: its largest magnitude sits at 2^14, and what falls below
+//            fp16's smallest step is 2^-38 of that);
+//   weights  P.V needs w_j = p_j 2^ev_j c_j: the power joins the exponent of the softmax weight,
+//            w_j = 2^(x_j + ev_j - m2 + 7) in fp16, with a running maximum m2 of x_j + ev_j of its
+//            own, apart from the maximum m1 that the sum of p_j = 2^(x_j - m1) is kept with. m2 moves
+//            only when it grows by more than 2^8, so w_j <= 2^15, and a weight is lost only below
+//            2^-32 of the largest.
+// Declared roundings: roped q to bf16, w to fp16 (2^-11 relative, each weight by itself), the output
+// to bf16; all sums are fp32.
+#include <math.h>
+
+#include "g4_kv8.cuh"
+
+namespace g4 {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kStages = 2;             // pages in flight per warp
+constexpr float kLazy = 8.0f;          // m2 moves when the maximum grows by more than 2^8
+constexpr float kShift = 7.0f;         // the weights' scale: w <= 2^(kLazy + kShift)
+constexpr float kNone = -1.0e38f;      // running maximum before the first key (finite: no inf - inf)
+
+template <bool GLOBAL>
+struct Shape {
+  using Blk = Kv8Block<GLOBAL>;
+  static constexpr int D = Blk::D;
+  static constexpr int kSegs = D / 128;                  // 128-column segments of V
+  static constexpr int kHalves = GLOBAL ? 8 : 4;         // 64-column halves of K: global 6 plain + 2 turned
+  static constexpr int kHeads = GLOBAL ? 8 : 2;          // at most; columns beyond the group carry q = 0
+  static constexpr int kChunk = GLOBAL ? kDecodeChunkGlobal : kDecodeChunkSliding;
+  static constexpr int kStage = (Blk::kBytes + 127) / 128 * 128;
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kQ = kHalves * 1024;              // q fragments: [half][2][32 lanes][16 bytes]
+  static constexpr int kSmem = kRing + kQ;
+  static_assert(kRing >= kWarps * kHeads * D * 4, "the warp merge reuses the ring");
+};
+
+struct Decode8Params {
+  const __nv_bfloat16* q;
+  const int32_t* seq_len;
+  const int32_t* pos;   // RoPE position of the query; NULL: seq_len - 1
+  int B;
+  int window;
+  float scale_log2;
+  PagedCache8 cache;
+  float* ws_ml;         // [B][hq][NC][2]: running max (log2 units) and sum
+  float* ws_o;          // [B][hq][NC][D]: un-normalised output, relative to that max
+  float* ws_page;       // [B][hkv][max_pages][8]: log2 of each page's weight, or NULL
+  int NC;
+  RopeTables tb;
+  uint32_t* err;
+  unsigned long long wait_ns;
+};
+
+// Two bytes of `w` (at the selector's places) as the fp16 pair of their codes.
+G4_DEV uint32_t codes2(uint32_t w, uint32_t selector) {
+  const uint32_t raw = __byte_perm(w, 0x64646464u, selector);   // 0x6400 | byte: 1024 + byte
+  const uint32_t bias = 0x64806480u;                            // 1152
+  __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&raw), *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<uint32_t*>(&d);
+}
+G4_DEV uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+G4_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
+      "%1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+G4_DEV uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+G4_DEV uint32_t pack_f16(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Position checks shared by the three kernels: the held index of request b's token, or -1.
+G4_DEV int held_index(const int32_t* seq_len, const int32_t* pos, int b, int max_pages, int& rope_pos) {
+  const int idx = seq_len[b] - 1;
+  rope_pos = pos ? pos[b] : idx;
+  return (idx < 0 || idx >= kMaxPos || (idx >> 4) >= max_pages || rope_pos < idx || rope_pos >= kMaxPos) ? -1 : idx;
+}
+
+// Column d of a query head -> which half of the K order it belongs to (see Shape::kHalves).
+template <bool GLOBAL>
+G4_DEV int half_of(int d) {
+  const int sh = d >> 6;
+  if (!GLOBAL) return sh;
+  return sh == 0 ? 6 : sh == 4 ? 7 : sh < 4 ? sh - 1 : sh - 2;
+}
+
+template <bool GLOBAL, bool PAGES>
+__global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode8Params p) {
+  using S = Shape<GLOBAL>;
+  using Blk = Kv8Block<GLOBAL>;
+  constexpr int D = S::D;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* q_s = smem + S::kRing;
+  __shared__ uint64_t full[kWarps][kStages];
+  __shared__ int abort_flag;
+  __shared__ float q_scale[8];
+  __shared__ float red_m[kWarps][8], red_l[kWarps][8], red_m2[kWarps][8];
+
+  const int HKV = p.cache.hkv, G = p.cache.hq / HKV;
+  const int cr = blockIdx.x % p.NC;                    // chunk slot, KV head, request
+  const int g = (blockIdx.x / p.NC) % HKV;
+  const int b = blockIdx.x / p.NC / HKV;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gq = lane >> 2, cq = lane & 3;             // matrix fragment coordinates
+
+  int rope_pos;
+  const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
+  if (last < 0) {
+    if (threadIdx.x == 0 && cr == 0 && g == 0) set_error(p.err, kErrPos);
+    return;   // the merge writes zeros for this request
+  }
+  const int lo = GLOBAL ? 0 : max(0, last - p.window + 1);
+  const int c = lo / S::kChunk + cr;
+  const int k_begin = max(lo, c * S::kChunk);
+  const int k_end = min(last, c * S::kChunk + S::kChunk - 1);   // inclusive
+  if (k_begin > k_end) return;                                    // unused slot
+
+  // This warp's pages: warp, warp + 4, ... of the chunk's; lane n keeps the n-th one's physical page.
+  const int pg0 = k_begin >> 4, n_pages = (k_end >> 4) - pg0 + 1;
+  const int mine = n_pages > warp ? (n_pages - warp + kWarps - 1) / kWarps : 0;   // at most 16
+  int phys = 0;
+  if (lane < mine) phys = p.cache.page_table[(size_t)b * p.cache.max_pages + pg0 + warp + kWarps * lane];
+  const bool bad = lane < mine && (phys < 0 || phys >= p.cache.num_pages);
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane < kStages) mbar_init(&full[warp][lane], 1);
+  fence_mbar_init();
+  const size_t slot = ((size_t)b * p.cache.hq + (size_t)G * g) * p.NC + cr;   // head G g + h adds h NC
+  if (__syncthreads_or(bad)) {   // a page outside the pool: this chunk adds nothing
+    if (threadIdx.x == 0) set_error(p.err, kErrPage);
+    if ((int)threadIdx.x < G) {
+      p.ws_ml[(slot + (size_t)threadIdx.x * p.NC) * 2 + 0] = -INFINITY;
+      p.ws_ml[(slot + (size_t)threadIdx.x * p.NC) * 2 + 1] = 0.f;
+    }
+    if (PAGES)
+      for (int i = threadIdx.x; i < n_pages * 8; i += kWarps * 32)
+        p.ws_page[(((size_t)b * HKV + g) * p.cache.max_pages + pg0) * 8 + i] = -INFINITY;
+    return;
+  }
+
+  uint8_t* ring = smem + warp * kStages * S::kStage;
+  auto issue = [&](int n, int page) {   // lane 0: copy this warp's n-th page
+    const int st = n % kStages;
+    mbar_arrive_expect_tx(&full[warp][st], Blk::kBytes);
+    bulk_g2s(ring + st * S::kStage, p.cache.pages + ((size_t)page * HKV + g) * Blk::kBytes, Blk::kBytes,
+             &full[warp][st]);
+  };
+#pragma unroll
+  for (int n = 0; n < kStages; ++n) {
+    const int page = __shfl_sync(0xffffffffu, phys, n);
+    if (lane == 0 && n < mine) issue(n, page);
+  }
+
+  // The query heads of this KV head, turned, cast to bf16, scaled by a power of two each and laid out
+  // as matrix fragments: lane (head, cc) of half i and step t holds columns 16 cc + 4t + {0, 2} and
+  // {1, 3} of the half. One warp per head.
+  for (int h = warp; h < 8; h += kWarps) {
+    constexpr int P = D / 64;   // pairs per lane
+    const int t0 = lane * P;
+    float a[P], bb[P];
+    if (h < G) {
+      const __nv_bfloat16* src = p.q + ((size_t)b * p.cache.hq + (size_t)G * g + h) * D;
+#pragma unroll
+      for (int i = 0; i < P; i += 2) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(src + t0 + i);
+        const uint32_t y = *reinterpret_cast<const uint32_t*>(src + D / 2 + t0 + i);
+        a[i] = bf16_lo(x);
+        a[i + 1] = bf16_hi(x);
+        bb[i] = bf16_lo(y);
+        bb[i + 1] = bf16_hi(y);
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (t0 < Blk::R) rope_pair(a[i], bb[i], rope_cs(p.tb, t0 + i, rope_pos));
+        a[i] = round_bf16(a[i]);   // declared cast: roped q in bf16
+        bb[i] = round_bf16(bb[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) a[i] = bb[i] = 0.f;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      m = max(m, max(__float_as_uint(a[i]) & 0x7fffffffu, __float_as_uint(bb[i]) & 0x7fffffffu));
+    m = __reduce_max_sync(0xffffffffu, m);
+    // largest |q| = 2^(eb - 127) up to twice that, moved to [2^14, 2^15); an infinity or NaN stays one
+    const int eb = max(20, min(254, (int)(m >> 23)));
+    const float down = __uint_as_float((uint32_t)(268 - eb) << 23);   // 2^(141 - eb)
+    if (lane == 0) q_scale[h] = __uint_as_float((uint32_t)(eb - 14) << 23);   // 2^(eb - 141)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int d = t0 + i + half * (D / 2);
+        const int dd = d & 63, cc = dd >> 4, t = (dd >> 2) & 3, e = dd & 3;
+        uint8_t* dst = q_s + ((half_of<GLOBAL>(d) * 2 + (t >> 1)) * 32 + h * 4 + cc) * 16 + (t & 1) * 8 + (e & 1) * 4 +
+                       (e >> 1) * 2;
+        *reinterpret_cast<__half*>(dst) = __float2half_rn((half ? bb[i] : a[i]) * down);
+      }
+    }
+  }
+  __syncthreads();
+  const float qs[2] = {q_scale[2 * cq] * p.scale_log2, q_scale[2 * cq + 1] * p.scale_log2};
+
+  float o[S::kSegs * 8][4];   // O^T: rows = columns of V, columns = heads 2cq, 2cq + 1
+#pragma unroll
+  for (int i = 0; i < S::kSegs * 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m1[2] = {kNone, kNone}, l1[2] = {0.f, 0.f}, m2[2] = {kNone, kNone};   // m1, l1 of this lane's own keys
+
+  const uint32_t q_addr = smem_u32(q_s) + lane * 16;
+  const uint32_t k_lane = gq * 128 + ((cq ^ kv8_swizzle(gq)) << 4);          // rows of K: key gq, piece cq (+ 4: ^ 64)
+  // columns of V: keys 2cq, 2cq + 1 (and + 8, 1 KB on), piece gq
+  const uint32_t v_lane0 = 2 * cq * 128 + ((gq ^ kv8_swizzle(2 * cq)) << 4);
+  const uint32_t v_lane1 = (2 * cq + 1) * 128 + ((gq ^ kv8_swizzle(2 * cq + 1)) << 4);
+
+  int n = 0;
+  for (; n < mine; ++n) {
+    const int st = n % kStages;
+    const bool ok = mbar_wait(&full[warp][st], (n / kStages) & 1, &abort_flag, p.err, p.wait_ns);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    const uint8_t* blk = ring + st * S::kStage;
+    const uint32_t base = smem_u32(blk);
+    const int key0 = (pg0 + warp + kWarps * n) * kPage;
+
+    // ---- S^T = K q^T: 16 keys x 8 heads, the plain and the turned columns apart, two chains each
+    float s0[2][4] = {}, s1[2][4] = {};
+#pragma unroll
+    for (int i = 0; i < S::kHalves; ++i) {
+      const bool turned = GLOBAL && i >= 6;
+      const int sh = !GLOBAL ? i : i < 3 ? i + 1 : i + 2;   // 64-column half of the tile
+      const uint32_t at = turned ? (uint32_t)Blk::kTile1 + (k_lane ^ (i == 7 ? 64u : 0u))
+                                 : (uint32_t)(sh >> 1) * 2048 + (k_lane ^ ((sh & 1) ? 64u : 0u));
+      const uint4 x = lds128(base + at), y = lds128(base + at + 1024);
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        const uint4 qf = lds128(q_addr + (i * 2 + tt) * 512);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int t = tt * 2 + u;
+          const uint32_t a0 = codes2(xw[t], 0x4240), a1 = codes2(yw[t], 0x4240);
+          const uint32_t a2 = codes2(xw[t], 0x4341), a3 = codes2(yw[t], 0x4341);
+          mma_f16(turned ? s1[u] : s0[u], a0, a1, a2, a3, u ? qf.z : qf.x, u ? qf.w : qf.y);
+        }
+      }
+    }
+
+    // ---- softmax of this lane's keys gq, gq + 8 for heads 2cq, 2cq + 1
+    const uint32_t e_lo = blk[Blk::kExp0 + gq], e_hi = blk[Blk::kExp0 + gq + 8];
+    const uint32_t f_lo = blk[Blk::kExp1 + gq], f_hi = blk[Blk::kExp1 + gq + 8];
+    const uint32_t v_lo = GLOBAL ? e_lo : f_lo, v_hi = GLOBAL ? e_hi : f_hi;
+    const float ev_lo = v_lo == 255u ? NAN : (float)((int)v_lo - 133), ev_hi = v_hi == 255u ? NAN : (float)((int)v_hi - 133);
+    const bool see_lo = key0 + gq >= k_begin && key0 + gq <= k_end;
+    const bool see_hi = key0 + gq + 8 >= k_begin && key0 + gq + 8 <= k_end;
+    float x[4], y[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float s = (s0[0][r] + s0[1][r]) * kv8_step(r < 2 ? e_lo : e_hi);
+      if (GLOBAL) s += (s1[0][r] + s1[1][r]) * kv8_step(r < 2 ? f_lo : f_hi);
+      const bool see = r < 2 ? see_lo : see_hi;
+      x[r] = see ? s * qs[r & 1] : -INFINITY;
+      y[r] = see ? x[r] + (r < 2 ? ev_lo : ev_hi) : -INFINITY;
+    }
+    float page_lse[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float mn = fmaxf(m1[j], fmaxf(x[j], x[2 + j]));
+      if (PAGES) {   // the page's weight by itself: its maximum and sum over the warp
+        float mp = fmaxf(x[j], x[2 + j]);
+#pragma unroll
+        for (int w = 4; w <= 16; w <<= 1) mp = fmaxf(mp, __shfl_xor_sync(0xffffffffu, mp, w));
+        mp = fmaxf(mp, kNone);
+        const float pa = ex2(x[j] - mp), pb = ex2(x[2 + j] - mp);
+        float ps = pa + pb;
+#pragma unroll
+        for (int w = 4; w <= 16; w <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, w);
+        page_lse[j] = mp + __log2f(ps);
+      }
+      l1[j] = fmaf(l1[j], ex2(m1[j] - mn), ex2(x[j] - mn) + ex2(x[2 + j] - mn));
+      m1[j] = mn;
+    }
+    if (PAGES && gq == 0)
+      *reinterpret_cast<float2*>(p.ws_page + (((size_t)b * HKV + g) * p.cache.max_pages + (key0 >> 4)) * 8 + 2 * cq) =
+          make_float2(page_lse[0], page_lse[1]);
+    // the weights' reference: moved (for the whole column) only when some key passes it by 2^8
+    const bool grow = fmaxf(y[0], y[2]) > m2[0] + kLazy || fmaxf(y[1], y[3]) > m2[1] + kLazy;
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float mn = fmaxf(y[j], y[2 + j]);
+#pragma unroll
+        for (int w = 4; w <= 16; w <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+        mn = fmaxf(mn, m2[j]);
+        const float al = ex2(m2[j] - mn);
+        m2[j] = mn;
+#pragma unroll
+        for (int i = 0; i < S::kSegs * 8; ++i) {
+          o[i][j] *= al;
+          o[i][2 + j] *= al;
+        }
+      }
+    }
+    float wgt[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) wgt[r] = ex2(y[r] - m2[r & 1] + kShift);
+    const uint32_t b0 = transpose8x8(pack_f16(wgt[0], wgt[1]));   // keys 2cq, 2cq + 1 of head gq
+    const uint32_t b1 = transpose8x8(pack_f16(wgt[2], wgt[3]));   // keys 2cq + 8, 2cq + 9
+
+    // ---- O^T += V^T w^T: columns 16 gq .. + 15 of each segment, keys 2cq, 2cq + 1, 2cq + 8, 2cq + 9
+#pragma unroll
+    for (int sg = 0; sg < S::kSegs; ++sg) {
+      const uint32_t at = base + (GLOBAL ? 0u : (uint32_t)Blk::kTile1) + sg * 2048;
+      const uint4 k0 = lds128(at + v_lane0), k1 = lds128(at + v_lane1);
+      const uint4 k2 = lds128(at + v_lane0 + 1024), k3 = lds128(at + v_lane1 + 1024);
+      const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+      const uint32_t w2[4] = {k2.x, k2.y, k2.z, k2.w}, w3[4] = {k3.x, k3.y, k3.z, k3.w};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        // byte pairs (key, key + 1) of columns 4t, 4t + 1 and of 4t + 2, 4t + 3
+        const uint32_t ab = __byte_perm(w0[t], w1[t], 0x5140), cd = __byte_perm(w0[t], w1[t], 0x7362);
+        const uint32_t ef = __byte_perm(w2[t], w3[t], 0x5140), gh = __byte_perm(w2[t], w3[t], 0x7362);
+        mma_f16(o[sg * 8 + 2 * t], codes2(ab, 0x4140), codes2(ab, 0x4342), codes2(ef, 0x4140), codes2(ef, 0x4342), b0, b1);
+        mma_f16(o[sg * 8 + 2 * t + 1], codes2(cd, 0x4140), codes2(cd, 0x4342), codes2(gh, 0x4140), codes2(gh, 0x4342), b0,
+                b1);
+      }
+    }
+    __syncwarp();
+    const int page = __shfl_sync(0xffffffffu, phys, (n + kStages) & 31);
+    if (lane == 0 && n + kStages < mine) {   // every lane has read the stage: refill it
+      fence_proxy_async();
+      issue(n + kStages, page);
+    }
+  }
+  if (n < mine && lane == 0) {   // a wait ran out: let the copies in flight finish (bounded)
+    const unsigned long long t0 = globaltimer();
+    for (int i = n; i < min(mine, n + kStages); ++i)
+      while (!mbar_try_wait(smem_u32(&full[warp][i % kStages]), (i / kStages) & 1) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+  }
+
+  // This warp's (m1, l1) per head, over the eight lanes that hold its keys.
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float mw = m1[j];
+#pragma unroll
+    for (int w = 4; w <= 16; w <<= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, w));
+    float lw = l1[j] * ex2(m1[j] - mw);
+#pragma unroll
+    for (int w = 4; w <= 16; w <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, w);
+    if (gq == 0) {
+      red_m[warp][2 * cq + j] = mw;
+      red_l[warp][2 * cq + j] = lw;
+      red_m2[warp][2 * cq + j] = m2[j];
+    }
+  }
+  __syncthreads();   // every stage has been read: reuse the ring for the warp merge
+  float* red_o = reinterpret_cast<float*>(smem);   // [warps][kHeads][D]
+#pragma unroll
+  for (int i = 0; i < S::kSegs * 8; ++i) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int d = (i >> 3) * 128 + gq * 16 + 2 * (i & 7) + (r >> 1), h = 2 * cq + (r & 1);
+      if (h < S::kHeads) red_o[(warp * S::kHeads + h) * D + d] = o[i][r];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
+    const int h = i / D, d = i % D;
+    float M = red_m[0][h];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, red_m[w][h]);
+    float L = 0.f, O = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      L = fmaf(red_l[w][h], ex2(red_m[w][h] - M), L);
+      const float f = ex2(0.5f * (red_m2[w][h] - kShift - M));   // its square may lie below 2^-126
+      O = fmaf(red_o[(w * S::kHeads + h) * D + d] * f, f, O);
+    }
+    const size_t s = slot + (size_t)h * p.NC;
+    p.ws_o[s * D + d] = O;
+    if (d == 0) {
+      p.ws_ml[s * 2 + 0] = L == 0.f ? -INFINITY : M;
+      p.ws_ml[s * 2 + 1] = L;
+    }
+  }
+}
+
+// Number of chunk slots that request b fills.
+G4_DEV int chunks_of(int last, int window, int chunk) {
+  const int lo = window > 0 ? max(0, last - window + 1) : 0;
+  return last / chunk - lo / chunk + 1;
+}
+
+// ---- ordered merge of the chunks: one block per (head, request), zeros for a refused request
+template <int D>
+__global__ void __launch_bounds__(D / 4) kv8_merge_kernel(const Decode8Params p, int chunk, __nv_bfloat16* out) {
+  const int h = blockIdx.x % p.cache.hq, b = blockIdx.x / p.cache.hq;
+  const int d0 = threadIdx.x * 4;
+  int rope_pos;
+  const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
+  const int n = last < 0 ? 0 : min(p.NC, chunks_of(last, p.window, chunk));
+  const size_t s0 = ((size_t)b * p.cache.hq + h) * p.NC;
+  float M = -INFINITY;
+  for (int c = 0; c < n; ++c) M = fmaxf(M, p.ws_ml[(s0 + c) * 2]);
+  float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (M != -INFINITY) {
+    for (int c = 0; c < n; ++c) {
+      const float mc = p.ws_ml[(s0 + c) * 2];
+      if (mc == -INFINITY) continue;   // a chunk that added nothing: its output slot was not written
+      const float w = ex2(mc - M);
+      L = fmaf(p.ws_ml[(s0 + c) * 2 + 1], w, L);
+      const float4 ov = *reinterpret_cast<const float4*>(p.ws_o + (s0 + c) * D + d0);
+      acc[0] = fmaf(ov.x, w, acc[0]);
+      acc[1] = fmaf(ov.y, w, acc[1]);
+      acc[2] = fmaf(ov.z, w, acc[2]);
+      acc[3] = fmaf(ov.w, w, acc[3]);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : __frcp_rn(L);
+  uint2 pk;
+  pk.x = pack_bf16(acc[0] * inv, acc[1] * inv);
+  pk.y = pack_bf16(acc[2] * inv, acc[3] * inv);
+  *reinterpret_cast<uint2*>(out + ((size_t)b * p.cache.hq + h) * D + d0) = pk;
+}
+
+// ---- accumulated page weights: page_weights[b][i] += sum over heads of the page's share of the softmax
+constexpr int kPageThreads = 256;
+__global__ void __launch_bounds__(kPageThreads) kv8_page_weights_kernel(const Decode8Params p, int chunk,
+                                                                        int blocks_per_row, float* page_weights) {
+  __shared__ float ref[kSlidingHq];   // log2 of each head's softmax sum: max + log2(L)
+  const int b = blockIdx.x / blocks_per_row, i0 = (blockIdx.x % blocks_per_row) * kPageThreads;
+  int rope_pos;
+  const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
+  const int n_pages = (last >> 4) + 1;   // 0 when refused
+  if (i0 >= n_pages) return;
+  const int HKV = p.cache.hkv, G = p.cache.hq / HKV;
+  const int n = min(p.NC, chunks_of(last, 0, chunk));
+  for (int h = threadIdx.x >> 5; h < p.cache.hq; h += kPageThreads / 32) {
+    const float* ml = p.ws_ml + ((size_t)b * p.cache.hq + h) * p.NC * 2;
+    const int lane = threadIdx.x & 31;
+    float M = -INFINITY;
+    for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[2 * c]);
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    float L = 0.f;
+    if (M != -INFINITY)
+      for (int c = lane; c < n; c += 32) L = fmaf(ml[2 * c + 1], ex2(ml[2 * c] - M), L);
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
+    if (lane == 0) ref[h] = M == -INFINITY ? INFINITY : M + log2f(L);   // no key: every share is 0
+  }
+  __syncthreads();
+  const int i = i0 + threadIdx.x;
+  if (i >= n_pages) return;
+  float sum = 0.f;
+  for (int g = 0; g < HKV; ++g) {
+    const float4* src = reinterpret_cast<const float4*>(p.ws_page + (((size_t)b * HKV + g) * p.cache.max_pages + i) * 8);
+    const float4 a = src[0], c = src[1];
+    const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < G) sum += ex2(v[h] - ref[G * g + h]);
+  }
+  page_weights[(size_t)b * p.cache.max_pages + i] += sum;
+}
+
+int chunk_slots(bool global, int max_pages, int window) {
+  const long long keys = (long long)max_pages * kPage < kMaxPos ? (long long)max_pages * kPage : kMaxPos;
+  if (global) return (int)((keys + kDecodeChunkGlobal - 1) / kDecodeChunkGlobal);
+  const int by_window = (window - 1) / kDecodeChunkSliding + 2;
+  const int by_table = (int)((keys + kDecodeChunkSliding - 1) / kDecodeChunkSliding);
+  return by_window < by_table ? by_window : by_table;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <bool GLOBAL, bool PAGES>
+cudaError_t launch(const Decode8Params& p, cudaStream_t s) {
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(kv8_decode_kernel<GLOBAL, PAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<GLOBAL>::kSmem);
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  const long long blocks = (long long)p.NC * p.cache.hkv * p.B;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  kv8_decode_kernel<GLOBAL, PAGES><<<(unsigned)blocks, kWarps * 32, Shape<GLOBAL>::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t kv8_decode_workspace_bytes(bool global, int B, int max_pages, int window, int hq, int hkv, bool pages) {
+  const size_t nc = (size_t)chunk_slots(global, max_pages, window);
+  const size_t D = global ? kGlobalD : kSlidingD;
+  size_t n = align256((size_t)B * hq * nc * 2 * sizeof(float)) + align256((size_t)B * hq * nc * D * sizeof(float));
+  if (pages) n += (size_t)B * hkv * max_pages * 8 * sizeof(float);
+  return n;
+}
+
+cudaError_t launch_kv8_decode(bool global, const void* q, const int32_t* seq_len, const int32_t* pos, int B, int window,
+                              float scale_log2, const PagedCache8& cache, float* page_weights, void* out, void* ws,
+                              const DeviceState& st, cudaStream_t s) {
+  if (B <= 0) return cudaSuccess;
+  Decode8Params p{};
+  p.q = (const __nv_bfloat16*)q;
+  p.seq_len = seq_len;
+  p.pos = pos;
+  p.B = B;
+  p.window = global ? 0 : window;
+  p.scale_log2 = scale_log2;
+  p.cache = cache;
+  p.NC = chunk_slots(global, cache.max_pages, window);
+  const size_t D = global ? kGlobalD : kSlidingD;
+  const size_t slots = (size_t)B * cache.hq * p.NC;
+  uint8_t* w = (uint8_t*)ws;
+  p.ws_ml = (float*)w;
+  w += align256(slots * 2 * sizeof(float));
+  p.ws_o = (float*)w;
+  w += align256(slots * D * sizeof(float));
+  p.ws_page = page_weights ? (float*)w : nullptr;
+  p.tb = global ? st.global : st.sliding;
+  p.err = st.err;
+  p.wait_ns = wait_limit_ns();
+  cudaError_t e;
+  if (!global)
+    e = launch<false, false>(p, s);
+  else
+    e = page_weights ? launch<true, true>(p, s) : launch<true, false>(p, s);
+  if (e != cudaSuccess) return e;
+  const long long heads = (long long)B * cache.hq;
+  if (heads > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int chunk = global ? kDecodeChunkGlobal : kDecodeChunkSliding;
+  if (global)
+    kv8_merge_kernel<kGlobalD><<<(unsigned)heads, kGlobalD / 4, 0, s>>>(p, chunk, (__nv_bfloat16*)out);
+  else
+    kv8_merge_kernel<kSlidingD><<<(unsigned)heads, kSlidingD / 4, 0, s>>>(p, chunk, (__nv_bfloat16*)out);
+  if ((e = cudaGetLastError()) != cudaSuccess || !page_weights) return e;
+  const int per_row = (cache.max_pages + kPageThreads - 1) / kPageThreads;
+  const long long rows = (long long)B * per_row;
+  if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
+  kv8_page_weights_kernel<<<(unsigned)rows, kPageThreads, 0, s>>>(p, chunk, per_row, page_weights);
+  return cudaGetLastError();
+}
+
+}  // namespace g4

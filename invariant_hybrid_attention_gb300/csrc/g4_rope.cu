@@ -797,6 +797,28 @@ cudaError_t launch_append_prefill(bool global, const void* k, const void* v, con
   return cudaGetLastError();
 }
 
+cudaError_t launch_stage_queries(bool global, const void* q, void* q_out, const SeqRows& rows, const PagedCache& cache,
+                                 const DeviceState& st, cudaStream_t s, const NormArgs& nm) {
+  if (rows.T <= 0 || rows.B <= 0) return cudaSuccess;
+  const unsigned blocks = (unsigned)((rows.T + 7) / 8);
+  const __nv_bfloat16* qb = (const __nv_bfloat16*)q;
+  __nv_bfloat16* qo = (__nv_bfloat16*)q_out;
+  const __nv_bfloat16* none = nullptr;
+  if (global && nm.any())
+    append_prefill_kernel<kGlobalD, kGlobalR, true, true>
+        <<<blocks, 256, 0, s>>>(none, none, qb, qo, rows, cache, st.global, st.err, nm, false);
+  else if (global)
+    append_prefill_kernel<kGlobalD, kGlobalR, true, false>
+        <<<blocks, 256, 0, s>>>(none, none, qb, qo, rows, cache, st.global, st.err, nm, false);
+  else if (nm.any())
+    append_prefill_kernel<kSlidingD, kSlidingR, false, true>
+        <<<blocks, 256, 0, s>>>(none, none, qb, qo, rows, cache, st.sliding, st.err, nm, false);
+  else
+    append_prefill_kernel<kSlidingD, kSlidingR, false, false>
+        <<<blocks, 256, 0, s>>>(none, none, qb, qo, rows, cache, st.sliding, st.err, nm, false);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_append_decode(bool global, const void* k_new, const void* v_new, const int32_t* seq_len,
                                  int B, const PagedCache& cache, const DeviceState& st, cudaStream_t s,
                                  const NormArgs& nm) {

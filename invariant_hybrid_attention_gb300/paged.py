@@ -10,7 +10,7 @@ from typing import Optional
 
 import torch
 
-from . import PAGE_SIZE, g4attn_cache, make_cache
+from . import PAGE_SIZE, g4attn_cache, g4attn_cache8, g4attn_kv8_page_bytes, make_cache, make_cache8
 
 
 ROT_DIMS = 128            # rotated columns of a global head: dims 0-63 and 256-319
@@ -88,6 +88,37 @@ class PagedKV:
 
     def nbytes(self) -> int:
         return sum(t.numel() * 2 for t in (self.k, self.v, self.k_rot) if t is not None)
+
+
+class PagedKV8:
+    """One layer's 8-bit paged cache: bytes [num_pages][n_kv_heads][block] (see include/g4attn.h)."""
+
+    def __init__(self, layer, num_pages: int, device="cuda", fill: Optional[int] = 255):
+        block = g4attn_kv8_page_bytes(layer) // int(layer.n_kv_heads)
+        self.pages = torch.empty((int(num_pages), int(layer.n_kv_heads), block), dtype=torch.uint8, device=device)
+        if fill is not None:
+            self.pages.fill_(fill)
+        self.num_pages = int(num_pages)
+
+    @property
+    def desc(self) -> g4attn_cache8:
+        return make_cache8(self.pages, self.num_pages)
+
+
+def untile8(pages: torch.Tensor, head_dim: int):
+    """The two tensors an 8-bit cache holds, as fp32 values [pages][heads][16][columns]: sliding K' and V,
+    global S and its 128 turned columns. Bytes [pages][heads][block] as in PagedKV8.pages."""
+    cols = (256, 256) if int(head_dim) == 256 else (512, ROT_DIMS)
+    j = torch.arange(PAGE_SIZE, device=pages.device)[:, None]
+    piece = torch.arange(8, device=pages.device)[None, :] ^ (j & 6) ^ ((j & 1) << 2)
+    out, at = [], 0
+    for i, n in enumerate(cols):
+        u = pages[..., at:at + PAGE_SIZE * n].unflatten(-1, (n // 128, PAGE_SIZE, 8, 16))[..., j, piece, :]
+        e = pages[..., PAGE_SIZE * (sum(cols) + i):PAGE_SIZE * (sum(cols) + i + 1)].int()
+        step = torch.where(e == 255, torch.full_like(e, 0x7FC00000), (e.clamp(8, 254) - 6) << 23).view(torch.float32)
+        out.append((u.transpose(-4, -3).flatten(-3).float() - 128.0) * step[..., None])
+        at += PAGE_SIZE * n
+    return out
 
 
 def device_int32(values, device="cuda") -> torch.Tensor:
