@@ -30,9 +30,9 @@ G4_DEV Vec<D> load_vec(const __nv_bfloat16* __restrict__ src, int t0) {
   return v;
 }
 
-// x / sqrt(mean(x^2) + eps), over the D/16 lanes of the vector.
+// x / sqrt(mean(x^2) + eps), over the D/16 lanes of the vector; returns the factor.
 template <int D>
-G4_DEV void unit_norm(Vec<D>& v, float eps) {
+G4_DEV float unit_norm(Vec<D>& v, float eps) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ss = fmaf(v.a[i], v.a[i], ss);
@@ -46,6 +46,7 @@ G4_DEV void unit_norm(Vec<D>& v, float eps) {
     v.a[i] *= inv;
     v.b[i] *= inv;
   }
+  return inv;
 }
 
 template <int D>
@@ -58,23 +59,36 @@ G4_DEV void weight(Vec<D>& v, const __nv_bfloat16* __restrict__ w, int t0) {
   }
 }
 
-// The largest |x| bits over the lanes of `mask` (all of which call it).
-template <int D>
-G4_DEV uint32_t max_bits(const Vec<D>& v, unsigned mask) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    m = max(m, max(__float_as_uint(v.a[i]) & 0x7fffffffu, __float_as_uint(v.b[i]) & 0x7fffffffu));
-  return __reduce_max_sync(mask, m);
+// max(a, |b|), NaN if either is one.
+G4_DEV float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
 }
 
-// Stores the vector as key j of a tile; col_b: the tile column of b[0].
+// The bits of the largest |x| over the lanes of `mask` (all of which call it); a NaN wins.
 template <int D>
-G4_DEV void store_vec(uint8_t* tile, uint8_t* exps, int j, const Vec<D>& v, int t0, int col_b, unsigned mask) {
+G4_DEV uint32_t max_bits(const Vec<D>& v, unsigned mask) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    m[0] = max_abs(m[0], v.a[i]);
+    m[1] = max_abs(m[1], v.a[i + 1]);
+    m[2] = max_abs(m[2], v.b[i]);
+    m[3] = max_abs(m[3], v.b[i + 1]);
+  }
+  return __reduce_max_sync(mask, __float_as_uint(max_abs(max_abs(m[0], m[1]), max_abs(m[2], m[3]))));
+}
+
+// Stores the vector as key j of a tile (off_a, off_b: the offsets of columns t0 and of b[0] there); the lane
+// of column 0 stores the exponent.
+template <int D>
+G4_DEV void store_vec(uint8_t* tile, uint32_t off_a, uint32_t off_b, uint8_t* exponent, const Vec<D>& v, bool first,
+                      unsigned mask) {
   const uint32_t e = kv8_exponent(max_bits<D>(v, mask));
-  *reinterpret_cast<uint2*>(tile + kv8_offset(j, t0)) = kv8_codes(v.a, e);
-  *reinterpret_cast<uint2*>(tile + kv8_offset(j, col_b)) = kv8_codes(v.b, e);
-  if (t0 == 0) exps[j] = (uint8_t)e;
+  *reinterpret_cast<uint2*>(tile + off_a) = kv8_codes(v.a, e);
+  *reinterpret_cast<uint2*>(tile + off_b) = kv8_codes(v.b, e);
+  if (first) *exponent = (uint8_t)e;
 }
 
 struct AppendArgs {
@@ -97,11 +111,13 @@ G4_DEV bool rows_ok(const SeqRows& r, int qs, int L, int cs) {
   return qs >= 0 && L <= r.T - qs && cs >= 0 && L <= kMaxPos && cs <= kMaxPos - L;
 }
 
-// One warp per (row, share of the KV heads). D/16 lanes per vector: two heads at a time when D = 256.
+// One warp per (row, share of the KV heads). The row's angles are computed once for its heads, in two-part
+// arithmetic. Sliding: half a warp per vector, two heads at a time, K' and V together. Global: a warp
+// per head for S, then 8 lanes per head for the turned columns of up to four heads at once.
 template <bool GLOBAL, bool NORM, int MODE>
 __global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs p) {
   using Blk = Kv8Block<GLOBAL>;
-  constexpr int D = Blk::D, R = Blk::R, LPV = D / 16, VPW = 32 / LPV;
+  constexpr int D = Blk::D, R = Blk::R, LPV = D / 16;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int n_rows = MODE == 0 ? p.rows.T : p.rows.B;
@@ -145,43 +161,68 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs p) {
     return;
   }
   const int j = idx & 15;
-  const int t0 = (lane % LPV) * 8;
-  float2 cs[8];
-  if (t0 < R) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = rope_cs(p.tb, t0 + i, pos);
-  }
-  const unsigned vec_mask = LPV == 32 ? 0xffffffffu : (0xffffu << (lane & 16));
-  const int HKV = p.cache.hkv;
-  const int per = (HKV + p.parts - 1) / p.parts;   // parts divides HKV / VPW, so this is exact
+  const int HKV = p.cache.hkv, per = HKV / p.parts, g_lo = part * per, g_hi = g_lo + per;
   uint8_t* page = p.cache.pages + (size_t)phys * HKV * Blk::kBytes;
-#pragma unroll 2
-  for (int g0 = part * per; g0 < (part + 1) * per; g0 += VPW) {
-    const int g = g0 + lane / LPV;
-    uint8_t* blk = page + (size_t)g * Blk::kBytes;
-    const size_t src = ((size_t)r * HKV + g) * D;
-    Vec<D> k = load_vec<D>(p.k + src, t0);
-    if (GLOBAL) {   // S as given (or n(S)), and the turned columns of K
-      if (NORM && p.nm.v_norm) unit_norm<D>(k, p.nm.eps);
-      store_vec<D>(blk, blk + Blk::kExp0, j, k, t0, D / 2 + t0, 0xffffffffu);
-      if (t0 < R) {
-        if (NORM && p.nm.wk) weight<D>(k, p.nm.wk, t0);
+  const __nv_bfloat16* k_row = p.k + (size_t)r * HKV * D;
+  const int tr = (lane % (R / 8)) * 8;   // this lane's turning pairs tr .. tr + 7
+  float2 cs[8];
+  {
+    const float4* cx = p.tb.coarse_x + (size_t)(pos >> 8) * R + tr;
+    const float4* fx = p.tb.fine_x + (size_t)(pos & 255) * R + tr;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rope_pair(k.a[i], k.b[i], cs[i]);
-        store_vec<D>(blk + Blk::kTile1, blk + Blk::kExp1, j, k, t0, R + t0, 0xffu);
+    for (int i = 0; i < 8; ++i) cs[i] = rope_cs_exact(__ldg(cx + i), __ldg(fx + i));
+  }
+  if (GLOBAL) {
+    const int t0 = lane * 8;
+    const uint32_t off_a = kv8_offset(j, t0), off_b = kv8_offset(j, D / 2 + t0);
+    float inv[4] = {1.f, 1.f, 1.f, 1.f};   // 1 / norm of each head (a full layer has four)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= per) break;
+      Vec<D> k = load_vec<D>(k_row + (size_t)(g_lo + i) * D, t0);
+      if (NORM && p.nm.v_norm) inv[i] = unit_norm<D>(k, p.nm.eps);
+      uint8_t* blk = page + (size_t)(g_lo + i) * Blk::kBytes;
+      store_vec<D>(blk, off_a, off_b, blk + Blk::kExp0 + j, k, lane == 0, 0xffffffffu);
+    }
+    const int i = lane >> 3;   // the turned columns of head g_lo + i
+    if (i < per) {
+      Vec<D> k = load_vec<D>(k_row + (size_t)(g_lo + i) * D, tr);
+      if (NORM) {
+        if (p.nm.v_norm) {
+          const float s = i == 0 ? inv[0] : i == 1 ? inv[1] : i == 2 ? inv[2] : inv[3];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            k.a[e] *= s;
+            k.b[e] *= s;
+          }
+        }
+        if (p.nm.wk) weight<D>(k, p.nm.wk, tr);
       }
-      __syncwarp();
-    } else {
-      Vec<D> v = load_vec<D>(p.v + src, t0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rope_pair(k.a[e], k.b[e], cs[e]);
+      uint8_t* blk = page + (size_t)(g_lo + i) * Blk::kBytes;
+      store_vec<D>(blk + Blk::kTile1, kv8_offset(j, tr), kv8_offset(j, R + tr), blk + Blk::kExp1 + j, k, tr == 0,
+                   0xffu << (lane & 24));
+    }
+  } else {
+    const int t0 = (lane % LPV) * 8;   // == tr
+    const uint32_t off_a = kv8_offset(j, t0), off_b = kv8_offset(j, D / 2 + t0);
+    const unsigned mask = 0xffffu << (lane & 16);
+    const __nv_bfloat16* v_row = p.v + (size_t)r * HKV * D;
+#pragma unroll 2
+    for (int g0 = g_lo; g0 < g_hi; g0 += 2) {
+      const int g = g0 + lane / LPV;
+      uint8_t* blk = page + (size_t)g * Blk::kBytes;
+      Vec<D> k = load_vec<D>(k_row + (size_t)g * D, t0), v = load_vec<D>(v_row + (size_t)g * D, t0);
       if (NORM && p.nm.wk) {
         unit_norm<D>(k, p.nm.eps);
         weight<D>(k, p.nm.wk, t0);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) rope_pair(k.a[i], k.b[i], cs[i]);
-      store_vec<D>(blk, blk + Blk::kExp0, j, k, t0, D / 2 + t0, vec_mask);
+      store_vec<D>(blk, off_a, off_b, blk + Blk::kExp0 + j, k, t0 == 0, mask);
       if (NORM && p.nm.v_norm) unit_norm<D>(v, p.nm.eps);
-      store_vec<D>(blk + Blk::kTile1, blk + Blk::kExp1, j, v, t0, D / 2 + t0, vec_mask);
+      store_vec<D>(blk + Blk::kTile1, off_a, off_b, blk + Blk::kExp1 + j, v, t0 == 0, mask);
     }
   }
 }
@@ -332,38 +373,17 @@ __global__ void __launch_bounds__(256) kv8_unpack_kernel(const UnpackArgs p) {
 }
 
 // ---- eviction: keep the first, the last and the heaviest pages ------------------------------------------
-// One block per sequence; its table row and weights stay in shared memory, so the outputs may be the
-// inputs. The n - keep lightest evictable pages leave: a radix select over the weights' ordered bits
-// (four passes of 8 bits) finds the weight of the last one to leave, T, and how many pages of weight
-// T leave; those are the first ones in index order. A block-wide scan then gives every page its place.
-constexpr int kEvictThreads = 1024;
-
-G4_DEV uint32_t ordered_bits(float w) {   // unsigned order = the order of the floats; NaN above all, or below if negative
+// One block per sequence, warp w and lane l hold pages (w * ITEMS + i) * 32 + l, i < ITEMS, in registers, so
+// the outputs may be the inputs. The n - keep lightest evictable pages leave. The weight T of the last
+// one to leave is found bit by bit from the top: the number of keys below a candidate is a compare per
+// key, a ballot-free warp sum and one barrier (the per-warp counts alternate between two arrays). Of
+// the pages of weight T the first in index order leave. Two block-wide scans of per-warp counts then
+// give every page its place.
+G4_DEV uint32_t ordered_bits(float w) {   // unsigned order = the order of the floats; NaN above all
   const uint32_t u = __float_as_uint(w);
+  if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
+  if ((u & 0x7fffffffu) == 0u) return 0x80000000u;   // -0 = 0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-// Exclusive sum over the block of one int per thread; *total gets the sum. sums: 32 ints.
-G4_DEV int block_scan(int x, int* sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  __syncthreads();   // sums may still be read from an earlier scan
-  if (lane == 31) sums[warp] = incl;
-  __syncthreads();
-  int s = sums[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += up;
-  }
-  *total = __shfl_sync(0xffffffffu, s, 31);
-  const int before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
-  return incl - x + (warp > 0 ? before : 0);
 }
 
 struct EvictArgs {
@@ -379,115 +399,118 @@ struct EvictArgs {
   uint32_t* err;
 };
 
-__global__ void __launch_bounds__(kEvictThreads) evict_pages_kernel(const EvictArgs p) {
-  extern __shared__ uint8_t smem[];
-  float* w = reinterpret_cast<float*>(smem);                   // [max_pages]
-  int32_t* tab = reinterpret_cast<int32_t*>(w + p.max_pages);  // [max_pages]
-  __shared__ int hist[256];
-  __shared__ int sums[32];
-  __shared__ uint32_t sel_prefix;
-  __shared__ int sel_left;
-  const int b = blockIdx.x, tid = threadIdx.x;
+template <int ITEMS>
+__global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
+  __shared__ int counts[2][32];
+  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
   const size_t row = (size_t)b * p.max_pages;
+  const int base = warp * ITEMS * 32 + lane;
+  float w[ITEMS];
+  int32_t tab[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {   // of the whole row: entries past the sequence's pages are not used
+    const int at = base + 32 * i;
+    w[i] = at < p.max_pages ? p.weights[row + at] : 0.f;
+    tab[i] = at < p.max_pages ? p.table[row + at] : -1;
+  }
   const int len = p.seq_len[b];
-  int n = 0;
-  if (len < 0 || len > kMaxPos || ((len + kPage - 1) >> 4) > p.max_pages) {
-    if (tid == 0) set_error(p.err, kErrPos);   // the row is passed on as it is
-    n = p.max_pages;
-  } else {
-    n = (len + kPage - 1) >> 4;
-  }
   const bool bad = len < 0 || len > kMaxPos || ((len + kPage - 1) >> 4) > p.max_pages;
+  const int n = bad ? p.max_pages : (len + kPage - 1) >> 4;   // a bad row is passed on as it is
   const int drop = bad ? 0 : max(0, n - p.keep);
-  for (int i = tid; i < n; i += kEvictThreads) {
-    w[i] = p.weights[row + i];
-    tab[i] = p.table[row + i];
+  const int e0 = p.first, e1 = n - p.last;   // evictable pages [e0, e1): at least drop, as keep >= first + last
+  // The sum over the block of one count per warp, in every thread; `round` alternates the arrays.
+  auto block_sum = [&](int x, int round) {
+    if (lane == 0) counts[round & 1][warp] = x;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, lane < n_warps ? counts[round & 1][lane] : 0);
+  };
+  // Exclusive sum over the warps before this one.
+  auto before = [&](int x, int round) {
+    if (lane == 0) counts[round & 1][warp] = x;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, lane < warp ? counts[round & 1][lane] : 0);
+  };
+  uint32_t key[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int at = base + 32 * i;
+    key[i] = at >= e0 && at < e1 ? ordered_bits(w[i]) : 0xffffffffu;
   }
-  if (tid == 0) {
-    sel_prefix = 0;
-    sel_left = drop;
-  }
-  __syncthreads();
-  const int e0 = p.first, e1 = n - p.last;   // evictable pages [e0, e1); drop <= e1 - e0 since keep >= first + last
+  uint32_t T = 0;     // the largest value with fewer than drop (+ 1) keys below it: the drop-th smallest key
+  int below = 0;      // keys below T
+  int round = 0;
   if (drop > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t prefix = sel_prefix;
-      for (int i = e0 + tid; i < e1; i += kEvictThreads) {
-        const uint32_t u = ordered_bits(w[i]);
-        // counting is exact in any order: these atomics decide nothing
-        if (shift == 24 || (u >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(u >> shift) & 255u], 1);
+    for (int bit = 31; bit >= 0; --bit, ++round) {
+      const uint32_t c = T | (1u << bit);
+      int x = 0;
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) x += key[i] < c ? 1 : 0;
+      x = block_sum(__reduce_add_sync(0xffffffffu, x), round);
+      if (x < drop) {
+        T = c;
+        below = x;
       }
-      __syncthreads();
-      if (tid == 0) {
-        int left = sel_left, d = 0;
-        while (left > hist[d]) left -= hist[d++];
-        sel_left = left;
-        sel_prefix = prefix | ((uint32_t)d << shift);
-      }
-      __syncthreads();
     }
   }
-  const uint32_t T = sel_prefix;   // pages below T leave, and the first `ties` of weight T
-  const int ties = sel_left;
-  int out_base = 0, tie_base = 0, ev_base = 0;
-  for (int i0 = 0; i0 < n; i0 += kEvictThreads) {
-    const int i = i0 + tid;
-    bool lower = false, tie = false;
-    if (drop > 0 && i >= e0 && i < e1) {
-      const uint32_t u = ordered_bits(w[i]);
-      lower = u < T;
-      tie = u == T;
-    }
-    int total;
-    const int t = tie_base + block_scan(tie ? 1 : 0, sums, &total);
-    tie_base += total;
-    const bool leaves = lower || (tie && t < ties);
-    const int ev = ev_base + block_scan(leaves ? 1 : 0, sums, &total);
-    if (i < n) {
-      if (leaves) {
+  const int ties = drop - below;   // pages of weight T that leave
+  unsigned tie_mask[ITEMS];
+  int x = 0;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int at = base + 32 * i;
+    tie_mask[i] = __ballot_sync(0xffffffffu, drop > 0 && at >= e0 && at < e1 && key[i] == T);
+    x += __popc(tie_mask[i]);
+  }
+  int tie = before(x, round++);
+  const unsigned lower = (1u << lane) - 1u;
+  unsigned leave[ITEMS];
+  x = 0;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const bool mine = (tie_mask[i] >> lane) & 1u;
+    const int at = base + 32 * i;
+    const bool out = drop > 0 && at >= e0 && at < e1 && (key[i] < T || (mine && tie + __popc(tie_mask[i] & lower) < ties));
+    tie += __popc(tie_mask[i]);
+    leave[i] = __ballot_sync(0xffffffffu, out);
+    x += __popc(leave[i]);
+  }
+  int gone = before(x, round);
+  const int kept = n - drop;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int at = base + 32 * i;
+    const int ev = gone + __popc(leave[i] & lower);   // evicted pages before this one
+    gone += __popc(leave[i]);
+    if (at < n) {
+      if ((leave[i] >> lane) & 1u) {
         p.freed[row + ev] = tab[i];
       } else {
-        const int to = out_base + tid - (ev - ev_base);
-        p.out_table[row + to] = tab[i];
-        p.out_weights[row + to] = w[i];
+        p.out_table[row + at - ev] = tab[i];
+        p.out_weights[row + at - ev] = w[i];
       }
     }
-    ev_base += total;
-    out_base += min(kEvictThreads, n - i0) - total;
+    if (at < p.max_pages) {   // what lies behind: none, none, no weight
+      if (at >= kept) {
+        p.out_table[row + at] = -1;
+        p.out_weights[row + at] = 0.f;
+      }
+      if (at >= drop) p.freed[row + at] = -1;
+    }
   }
-  const int kept = n - drop;
-  for (int i = kept + tid; i < p.max_pages; i += kEvictThreads) {
-    p.out_table[row + i] = -1;
-    p.out_weights[row + i] = 0.f;
-  }
-  for (int i = drop + tid; i < p.max_pages; i += kEvictThreads) p.freed[row + i] = -1;
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
+    if (bad) set_error(p.err, kErrPos);
     p.out_len[b] = bad ? len : len - kPage * drop;
     p.n_freed[b] = drop;
   }
 }
 
-// Raises the kernel's dynamic shared-memory limit once per device.
-template <class Kernel>
-cudaError_t allow_smem(Kernel kernel, int bytes, bool (&done)[64]) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!done[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    done[dev] = true;
-  }
-  return cudaSuccess;
-}
-
 template <bool GLOBAL, int MODE>
 cudaError_t append(AppendArgs& a, int n_rows, cudaStream_t s) {
-  constexpr int VPW = 32 / (Kv8Block<GLOBAL>::D / 16);
-  a.parts = a.cache.hkv / VPW;
+  // One warp per row computes its angles once for all heads; with few rows the heads are shared out
+  // so that about 32 warps run per SM (a row's bytes do not depend on it).
+  const int most = a.cache.hkv / (GLOBAL ? 1 : 2);
+  a.parts = 1;
+  while (a.parts < most && (long long)n_rows * a.parts < 152 * 32) a.parts *= 2;
   const long long blocks = ((long long)n_rows * a.parts + 7) / 8;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (a.nm.any())
@@ -533,13 +556,17 @@ cudaError_t launch_kv8_unpack(bool global, const Kv8Range& range, const PagedCac
 cudaError_t launch_evict_pages(const int32_t* seq_len, const int32_t* table, const float* weights, int B, int max_pages,
                                int keep, int first, int last, int32_t* out_len, int32_t* out_table, float* out_weights,
                                int32_t* freed, int32_t* n_freed, const DeviceState& st, cudaStream_t s) {
-  static bool done[64] = {};
-  const int bytes = max_pages * 8;
-  cudaError_t e = allow_smem(evict_pages_kernel, kMaxPos / kPage * 8, done);
-  if (e != cudaSuccess) return e;
   EvictArgs a{seq_len, table, weights, max_pages, keep, first, last, out_len, out_table, out_weights, freed, n_freed,
               st.err};
-  evict_pages_kernel<<<B, kEvictThreads, bytes, s>>>(a);
+  // Few pages per thread while that keeps the block small (its barriers are what a short row costs).
+  const int items = max_pages <= 1024 ? 2 : max_pages <= 4096 ? 4 : 16;
+  const unsigned threads = (unsigned)((max_pages + 32 * items - 1) / (32 * items) * 32);
+  if (items == 2)
+    evict_pages_kernel<2><<<B, threads, 0, s>>>(a);
+  else if (items == 4)
+    evict_pages_kernel<4><<<B, threads, 0, s>>>(a);
+  else
+    evict_pages_kernel<16><<<B, threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -59,16 +59,21 @@ G4_DEV uint32_t kv8_exponent(uint32_t max_bits) {
 // 1 / step for exponents 8 .. 254.
 G4_DEV float kv8_inverse_step(uint32_t biased) { return __uint_as_float((260u - biased) << 23); }
 
-// Eight consecutive columns as stored bytes (biased: the vector's exponent byte).
+// Eight consecutive columns as stored bytes (biased: the vector's exponent byte). x / step is exact;
+// adding 1.5 * 2^23 + 128 rounds it to a whole number, half to even, and leaves code + 128 in the
+// sum's low byte.
 G4_DEV uint2 kv8_codes(const float (&x)[8], uint32_t biased) {
   if (biased == 0u || biased == 255u) return make_uint2(0x80808080u, 0x80808080u);
-  const float inv = kv8_inverse_step(biased);
-  uint32_t w[2] = {0u, 0u};
+  const float inv = kv8_inverse_step(biased), mid = 12583040.0f;
+  uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = max(-127, min(127, __float2int_rn(x[i] * inv)));
-    w[i >> 2] |= (uint32_t)(c + 128) << (8 * (i & 3));
-  }
+  for (int i = 0; i < 8; ++i)
+    c[i] = __float_as_uint(fminf(fmaxf(fmaf(x[i], inv, mid), mid - 127.0f), mid + 127.0f));
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040),
+                       0x5410);
   return make_uint2(w[0], w[1]);
 }
 

@@ -3,10 +3,13 @@
 // merged in ascending chunk order; inside a chunk page i goes to warp i % 4 and the warps' states
 // merge in warp order. Every number a request gets depends on its own position, window and data.
 //
-// The stored bytes are codes u = 128 + c of values c 2^e with one exponent e per key and tile
-// (g4_kv8.cuh). The matrix instructions (m16n8k16, fp16 operands, fp32 sums) take the codes as they
-// are: 0x6400 | u is the fp16 number 1024 + u, and subtracting 1152 leaves c exactly. The powers of
-// two stay outside:
+// The stored bytes are u = c + 128 for values c 2^e with one exponent e per key and tile (g4_kv8.cuh).
+// The matrix instructions (m16n8k16, fp16 operands, fp32 sums) take the bytes as they are: 0x00uu is
+// the fp16 subnormal u 2^-24, which they multiply exactly, so one byte permute makes an operand pair.
+// The bias of 128 is taken off the sums: 128 sum(q) from the scores, and 128 sum(w) from the value
+// sums, where sum(w) is itself a row of that product (a row of constant bytes 128), so that what the
+// tensor cores' fp32 sums round away of the common part is rounded away on both sides. The
+// powers of two stay outside:
 //   scores   x_j = scale log2(e) 2^e_j (c_j . q), with q as fp16 scaled by a power of two per head
 //            (the bf16 q' is exact there: its largest magnitude sits at 2^14, and what falls below
 //            fp16's smallest step is 2^-38 of that);
@@ -63,13 +66,10 @@ struct Decode8Params {
   unsigned long long wait_ns;
 };
 
-// Two bytes of `w` (at the selector's places) as the fp16 pair of their codes.
-G4_DEV uint32_t codes2(uint32_t w, uint32_t selector) {
-  const uint32_t raw = __byte_perm(w, 0x64646464u, selector);   // 0x6400 | byte: 1024 + byte
-  const uint32_t bias = 0x64806480u;                            // 1152
-  __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&raw), *reinterpret_cast<const __half2*>(&bias));
-  return *reinterpret_cast<uint32_t*>(&d);
-}
+constexpr float kUp = 16777216.0f;   // 2^24: undoes the bytes' reading as fp16 subnormals
+
+// Two bytes of `w` as a pair of fp16 subnormals: the bytes at selector digits 0 and 2 (digit 4: zero).
+G4_DEV uint32_t codes2(uint32_t w, uint32_t selector) { return __byte_perm(w, 0u, selector); }
 G4_DEV uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -92,7 +92,12 @@ G4_DEV uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Position checks shared by the three kernels: the held index of request b's token, or -1.
+// Programmatic dependent launch: lets the next kernel of the stream start its blocks; waits for the
+// kernel before this one to finish and its writes to be visible.
+G4_DEV void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+G4_DEV void wait_for_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Position checks shared by the two kernels: the held index of request b's token, or -1.
 G4_DEV int held_index(const int32_t* seq_len, const int32_t* pos, int b, int max_pages, int& rope_pos) {
   const int idx = seq_len[b] - 1;
   rope_pos = pos ? pos[b] : idx;
@@ -116,9 +121,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   uint8_t* q_s = smem + S::kRing;
   __shared__ uint64_t full[kWarps][kStages];
   __shared__ int abort_flag;
-  __shared__ float q_scale[8];
+  __shared__ float q_scale[8], q_sum[2][8];   // per head: power of two, 128 x sum of q over the plain and turned columns
   __shared__ float red_m[kWarps][8], red_l[kWarps][8], red_m2[kWarps][8];
 
+  let_next_grid_start();
   const int HKV = p.cache.hkv, G = p.cache.hq / HKV;
   const int cr = blockIdx.x % p.NC;                    // chunk slot, KV head, request
   const int g = (blockIdx.x / p.NC) % HKV;
@@ -210,6 +216,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     const int eb = max(20, min(254, (int)(m >> 23)));
     const float down = __uint_as_float((uint32_t)(268 - eb) << 23);   // 2^(141 - eb)
     if (lane == 0) q_scale[h] = __uint_as_float((uint32_t)(eb - 14) << 23);   // 2^(eb - 141)
+    float sum = 0.f;   // a lane's columns are all plain or all turned
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      a[i] *= down;
+      bb[i] *= down;
+      sum += __half2float(__float2half_rn(a[i])) + __half2float(__float2half_rn(bb[i]));
+    }
+    const bool turned = GLOBAL && t0 < Blk::R;
+    float plain_sum = turned ? 0.f : sum, turned_sum = turned ? sum : 0.f;
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) {
+      plain_sum += __shfl_xor_sync(0xffffffffu, plain_sum, w);
+      if (GLOBAL) turned_sum += __shfl_xor_sync(0xffffffffu, turned_sum, w);
+    }
+    if (lane == 0) {
+      q_sum[0][h] = 128.0f * plain_sum;
+      q_sum[1][h] = 128.0f * turned_sum;
+    }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
 #pragma unroll
@@ -218,16 +242,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
         const int dd = d & 63, cc = dd >> 4, t = (dd >> 2) & 3, e = dd & 3;
         uint8_t* dst = q_s + ((half_of<GLOBAL>(d) * 2 + (t >> 1)) * 32 + h * 4 + cc) * 16 + (t & 1) * 8 + (e & 1) * 4 +
                        (e >> 1) * 2;
-        *reinterpret_cast<__half*>(dst) = __float2half_rn((half ? bb[i] : a[i]) * down);
+        *reinterpret_cast<__half*>(dst) = __float2half_rn(half ? bb[i] : a[i]);
       }
     }
   }
   __syncthreads();
   const float qs[2] = {q_scale[2 * cq] * p.scale_log2, q_scale[2 * cq + 1] * p.scale_log2};
+  const float q0[2] = {q_sum[0][2 * cq], q_sum[0][2 * cq + 1]}, q1[2] = {q_sum[1][2 * cq], q_sum[1][2 * cq + 1]};
 
   float o[S::kSegs * 8][4];   // O^T: rows = columns of V, columns = heads 2cq, 2cq + 1
 #pragma unroll
   for (int i = 0; i < S::kSegs * 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float ow[4] = {0.f, 0.f, 0.f, 0.f};   // the row of constant bytes 128
   float m1[2] = {kNone, kNone}, l1[2] = {0.f, 0.f}, m2[2] = {kNone, kNone};   // m1, l1 of this lane's own keys
 
   const uint32_t q_addr = smem_u32(q_s) + lane * 16;
@@ -245,8 +271,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     const uint32_t base = smem_u32(blk);
     const int key0 = (pg0 + warp + kWarps * n) * kPage;
 
-    // ---- S^T = K q^T: 16 keys x 8 heads, the plain and the turned columns apart, two chains each
-    float s0[2][4] = {}, s1[2][4] = {};
+    // ---- S^T = K q^T: 16 keys x 8 heads, the plain columns (four chains) and the turned ones (two) apart
+    float s0[4][4] = {}, s1[2][4] = {};
 #pragma unroll
     for (int i = 0; i < S::kHalves; ++i) {
       const bool turned = GLOBAL && i >= 6;
@@ -263,7 +289,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
           const int t = tt * 2 + u;
           const uint32_t a0 = codes2(xw[t], 0x4240), a1 = codes2(yw[t], 0x4240);
           const uint32_t a2 = codes2(xw[t], 0x4341), a3 = codes2(yw[t], 0x4341);
-          mma_f16(turned ? s1[u] : s0[u], a0, a1, a2, a3, u ? qf.z : qf.x, u ? qf.w : qf.y);
+          mma_f16(turned ? s1[u] : s0[t], a0, a1, a2, a3, u ? qf.z : qf.x, u ? qf.w : qf.y);
         }
       }
     }
@@ -278,8 +304,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     float x[4], y[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      float s = (s0[0][r] + s0[1][r]) * kv8_step(r < 2 ? e_lo : e_hi);
-      if (GLOBAL) s += (s1[0][r] + s1[1][r]) * kv8_step(r < 2 ? f_lo : f_hi);
+      const float sum0 = (s0[0][r] + s0[1][r]) + (s0[2][r] + s0[3][r]);
+      float s = fmaf(sum0, kUp, -q0[r & 1]) * kv8_step(r < 2 ? e_lo : e_hi);
+      if (GLOBAL) s += fmaf(s1[0][r] + s1[1][r], kUp, -q1[r & 1]) * kv8_step(r < 2 ? f_lo : f_hi);
       const bool see = r < 2 ? see_lo : see_hi;
       x[r] = see ? s * qs[r & 1] : -INFINITY;
       y[r] = see ? x[r] + (r < 2 ? ev_lo : ev_hi) : -INFINITY;
@@ -321,6 +348,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
           o[i][j] *= al;
           o[i][2 + j] *= al;
         }
+        ow[j] *= al;
       }
     }
     float wgt[4];
@@ -328,6 +356,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     for (int r = 0; r < 4; ++r) wgt[r] = ex2(y[r] - m2[r & 1] + kShift);
     const uint32_t b0 = transpose8x8(pack_f16(wgt[0], wgt[1]));   // keys 2cq, 2cq + 1 of head gq
     const uint32_t b1 = transpose8x8(pack_f16(wgt[2], wgt[3]));   // keys 2cq + 8, 2cq + 9
+
+    mma_f16(ow, 0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u, b0, b1);
 
     // ---- O^T += V^T w^T: columns 16 gq .. + 15 of each segment, keys 2cq, 2cq + 1, 2cq + 8, 2cq + 9
 #pragma unroll
@@ -383,7 +413,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int d = (i >> 3) * 128 + gq * 16 + 2 * (i & 7) + (r >> 1), h = 2 * cq + (r & 1);
-      if (h < S::kHeads) red_o[(warp * S::kHeads + h) * D + d] = o[i][r];
+      if (h < S::kHeads) red_o[(warp * S::kHeads + h) * D + d] = (o[i][r] - ow[r & 1]) * kUp;
     }
   }
   __syncthreads();
@@ -414,60 +444,100 @@ G4_DEV int chunks_of(int last, int window, int chunk) {
   return last / chunk - lo / chunk + 1;
 }
 
-// ---- ordered merge of the chunks: one block per (head, request), zeros for a refused request
-template <int D>
-__global__ void __launch_bounds__(D / 4) kv8_merge_kernel(const Decode8Params p, int chunk, __nv_bfloat16* out) {
-  const int h = blockIdx.x % p.cache.hq, b = blockIdx.x / p.cache.hq;
-  const int d0 = threadIdx.x * 4;
-  int rope_pos;
-  const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
-  const int n = last < 0 ? 0 : min(p.NC, chunks_of(last, p.window, chunk));
-  const size_t s0 = ((size_t)b * p.cache.hq + h) * p.NC;
-  float M = -INFINITY;
-  for (int c = 0; c < n; ++c) M = fmaxf(M, p.ws_ml[(s0 + c) * 2]);
-  float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  if (M != -INFINITY) {
-    for (int c = 0; c < n; ++c) {
-      const float mc = p.ws_ml[(s0 + c) * 2];
-      if (mc == -INFINITY) continue;   // a chunk that added nothing: its output slot was not written
-      const float w = ex2(mc - M);
-      L = fmaf(p.ws_ml[(s0 + c) * 2 + 1], w, L);
-      const float4 ov = *reinterpret_cast<const float4*>(p.ws_o + (s0 + c) * D + d0);
-      acc[0] = fmaf(ov.x, w, acc[0]);
-      acc[1] = fmaf(ov.y, w, acc[1]);
-      acc[2] = fmaf(ov.z, w, acc[2]);
-      acc[3] = fmaf(ov.w, w, acc[3]);
-    }
-  }
-  const float inv = L == 0.f ? 0.f : __frcp_rn(L);
-  uint2 pk;
-  pk.x = pack_bf16(acc[0] * inv, acc[1] * inv);
-  pk.y = pack_bf16(acc[2] * inv, acc[3] * inv);
-  *reinterpret_cast<uint2*>(out + ((size_t)b * p.cache.hq + h) * D + d0) = pk;
-}
+// ---- ordered merge of the chunks, and the accumulated page weights -----------------------------------------
+// Blocks [0, merge_blocks) merge: one per (request, head, 128 columns). Chunk c's weight 2^(m_c - M) is
+// computed once, by lane c % 32; warp w then adds the chunks c = w (mod 4) in ascending order, eight
+// loads in flight, and the four sums are added in warp order: a tree fixed by the chunk numbers. A
+// refused request gets zeros. The other blocks add page_weights[b][i] += sum over heads of the page's
+// share of the softmax, a thread per page, heads in ascending order.
+// The kernel starts while the last chunk blocks run and waits for them before its first read
+// (programmatic dependent launch): its launch and the position look-ups cost no time of their own.
+constexpr int kFinishThreads = 128;
 
-// ---- accumulated page weights: page_weights[b][i] += sum over heads of the page's share of the softmax
-constexpr int kPageThreads = 256;
-__global__ void __launch_bounds__(kPageThreads) kv8_page_weights_kernel(const Decode8Params p, int chunk,
-                                                                        int blocks_per_row, float* page_weights) {
-  __shared__ float ref[kSlidingHq];   // log2 of each head's softmax sum: max + log2(L)
-  const int b = blockIdx.x / blocks_per_row, i0 = (blockIdx.x % blocks_per_row) * kPageThreads;
+template <int D, bool PAGES>
+__global__ void __launch_bounds__(kFinishThreads) kv8_finish_kernel(const Decode8Params p, int chunk, unsigned merge_blocks,
+                                                                    int blocks_per_row, __nv_bfloat16* out,
+                                                                    float* page_weights) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hq = p.cache.hq;
+  if (!PAGES || blockIdx.x < merge_blocks) {
+    __shared__ float4 part[3][32];
+    constexpr int kCols = D / 128;
+    const int col = (blockIdx.x % kCols) * 128 + lane * 4;
+    const int h = (blockIdx.x / kCols) % hq, b = blockIdx.x / kCols / hq;
+    int rope_pos;
+    const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
+    const int n = last < 0 ? 0 : min(p.NC, chunks_of(last, p.window, chunk));
+    const size_t s0 = ((size_t)b * hq + h) * p.NC;
+    wait_for_grid();
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + s0;
+    float M = -INFINITY;
+    for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[c].x);
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < n; c0 += 32) {
+      const float2 v = c0 + lane < n ? ml[c0 + lane] : make_float2(-INFINITY, 0.f);
+      const bool some = v.x != -INFINITY;   // a chunk that added nothing did not write its output slot
+      const float wc = some ? ex2(v.x - M) : 0.f;
+      if (some) L = fmaf(v.y, wc, L);
+      const unsigned wrote = __ballot_sync(0xffffffffu, some);
+      float4 o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = warp + 4 * i;
+        o[i] = ((wrote >> c) & 1u) ? *reinterpret_cast<const float4*>(p.ws_o + (s0 + c0 + c) * D + col)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = __shfl_sync(0xffffffffu, wc, warp + 4 * i);
+        acc.x = fmaf(o[i].x, w, acc.x);
+        acc.y = fmaf(o[i].y, w, acc.y);
+        acc.z = fmaf(o[i].z, w, acc.z);
+        acc.w = fmaf(o[i].w, w, acc.w);
+      }
+    }
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
+    if (warp > 0) part[warp - 1][lane] = acc;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w) {
+      const float4 q = part[w][lane];
+      acc.x += q.x;
+      acc.y += q.y;
+      acc.z += q.z;
+      acc.w += q.w;
+    }
+    const float inv = L == 0.f ? 0.f : __frcp_rn(L);
+    uint2 pk;
+    pk.x = pack_bf16(acc.x * inv, acc.y * inv);
+    pk.y = pack_bf16(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(out + ((size_t)b * hq + h) * D + col) = pk;
+    return;
+  }
+  __shared__ float ref[kSlidingHq];   // log2 of each head's softmax sum
+  const int unit = blockIdx.x - merge_blocks;
+  const int b = unit / blocks_per_row, i0 = (unit % blocks_per_row) * kFinishThreads;
   int rope_pos;
   const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
   const int n_pages = (last >> 4) + 1;   // 0 when refused
   if (i0 >= n_pages) return;
-  const int HKV = p.cache.hkv, G = p.cache.hq / HKV;
+  const int HKV = p.cache.hkv, G = hq / HKV;
   const int n = min(p.NC, chunks_of(last, 0, chunk));
-  for (int h = threadIdx.x >> 5; h < p.cache.hq; h += kPageThreads / 32) {
-    const float* ml = p.ws_ml + ((size_t)b * p.cache.hq + h) * p.NC * 2;
-    const int lane = threadIdx.x & 31;
+  wait_for_grid();
+  for (int h = warp; h < hq; h += kFinishThreads / 32) {
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)b * hq + h) * p.NC;
     float M = -INFINITY;
-    for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[2 * c]);
+    for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[c].x);
 #pragma unroll
     for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
     float L = 0.f;
     if (M != -INFINITY)
-      for (int c = lane; c < n; c += 32) L = fmaf(ml[2 * c + 1], ex2(ml[2 * c] - M), L);
+      for (int c = lane; c < n; c += 32) L = fmaf(ml[c].y, ex2(ml[c].x - M), L);
 #pragma unroll
     for (int w = 16; w >= 1; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
     if (lane == 0) ref[h] = M == -INFINITY ? INFINITY : M + log2f(L);   // no key: every share is 0
@@ -476,10 +546,11 @@ __global__ void __launch_bounds__(kPageThreads) kv8_page_weights_kernel(const De
   const int i = i0 + threadIdx.x;
   if (i >= n_pages) return;
   float sum = 0.f;
+#pragma unroll 4
   for (int g = 0; g < HKV; ++g) {
     const float4* src = reinterpret_cast<const float4*>(p.ws_page + (((size_t)b * HKV + g) * p.cache.max_pages + i) * 8);
-    const float4 a = src[0], c = src[1];
-    const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+    const float4 x = src[0], y = src[1];
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int h = 0; h < 8; ++h)
       if (h < G) sum += ex2(v[h] - ref[G * g + h]);
@@ -496,6 +567,25 @@ int chunk_slots(bool global, int max_pages, int window) {
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int D, bool PAGES>
+cudaError_t finish(const Decode8Params& p, int chunk, void* out, float* page_weights, cudaStream_t s) {
+  const long long merge_blocks = (long long)p.B * p.cache.hq * (D / 128);
+  const int per_row = (p.cache.max_pages + kFinishThreads - 1) / kFinishThreads;
+  const long long blocks = merge_blocks + (PAGES ? (long long)p.B * per_row : 0);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kFinishThreads);
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_finish_kernel<D, PAGES>, p, chunk, (unsigned)merge_blocks, per_row,
+                            (__nv_bfloat16*)out, page_weights);
+}
 
 template <bool GLOBAL, bool PAGES>
 cudaError_t launch(const Decode8Params& p, cudaStream_t s) {
@@ -556,19 +646,9 @@ cudaError_t launch_kv8_decode(bool global, const void* q, const int32_t* seq_len
   else
     e = page_weights ? launch<true, true>(p, s) : launch<true, false>(p, s);
   if (e != cudaSuccess) return e;
-  const long long heads = (long long)B * cache.hq;
-  if (heads > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const int chunk = global ? kDecodeChunkGlobal : kDecodeChunkSliding;
-  if (global)
-    kv8_merge_kernel<kGlobalD><<<(unsigned)heads, kGlobalD / 4, 0, s>>>(p, chunk, (__nv_bfloat16*)out);
-  else
-    kv8_merge_kernel<kSlidingD><<<(unsigned)heads, kSlidingD / 4, 0, s>>>(p, chunk, (__nv_bfloat16*)out);
-  if ((e = cudaGetLastError()) != cudaSuccess || !page_weights) return e;
-  const int per_row = (cache.max_pages + kPageThreads - 1) / kPageThreads;
-  const long long rows = (long long)B * per_row;
-  if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
-  kv8_page_weights_kernel<<<(unsigned)rows, kPageThreads, 0, s>>>(p, chunk, per_row, page_weights);
-  return cudaGetLastError();
+  if (!global) return finish<kSlidingD, false>(p, kDecodeChunkSliding, out, nullptr, s);
+  return page_weights ? finish<kGlobalD, true>(p, kDecodeChunkGlobal, out, page_weights, s)
+                      : finish<kGlobalD, false>(p, kDecodeChunkGlobal, out, nullptr, s);
 }
 
 }  // namespace g4
