@@ -127,6 +127,15 @@ G4_DEV float2 rope_cs(const RopeTables& tb, int t, int pos) {
   return cmul(cmul(c, m), f);
 }
 
+// rope_cs from the entry-major tables (R pairs per entry; the same bits): for lanes that hold
+// consecutive pairs.
+G4_DEV float2 rope_cs_t(const RopeTables& tb, int R, int t, int pos) {
+  const float2 c = __ldg(tb.coarse_t + (size_t)(pos >> 8) * R + t);
+  const float2 m = __ldg(tb.mid_t + ((pos >> 4) & 15) * R + t);
+  const float2 f = __ldg(tb.fine_t + (pos & 15) * R + t);
+  return cmul(cmul(c, m), f);
+}
+
 // a b - c d and its kind in two fp32 parts: products exact through fma, the sum's error kept, one rounding
 // at the end.
 G4_DEV float dot2_exact(float ah, float al, float bh, float bl, float ch, float cl, float dh, float dl) {

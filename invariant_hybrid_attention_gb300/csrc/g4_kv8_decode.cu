@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   __shared__ uint64_t full[kWarps][kStages];
   __shared__ int abort_flag;
   __shared__ float q_scale[8], q_sum[2][8];   // per head: power of two, 128 x sum of q over the plain and turned columns
-  __shared__ float red_m[kWarps][8], red_l[kWarps][8], red_m2[kWarps][8];
+  __shared__ float red_m[kWarps][8], red_l[kWarps][8], red_m2[kWarps][8], factor[kWarps][8];
 
   let_next_grid_start();
   const int HKV = p.cache.hkv, G = p.cache.hq / HKV;
@@ -182,24 +182,35 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   // The query heads of this KV head, turned, cast to bf16, scaled by a power of two each and laid out
   // as matrix fragments: lane (head, cc) of half i and step t holds columns 16 cc + 4t + {0, 2} and
   // {1, 3} of the half. One warp per head.
+  constexpr int P = D / 64;   // pairs per lane
+  const int t0 = lane * P;
+  float2 cs[P];               // (cos, sin) of this lane's pairs, the same for every head
+  if (t0 < Blk::R) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) cs[i] = rope_cs_t(p.tb, Blk::R, t0 + i, rope_pos);
+  }
   for (int h = warp; h < 8; h += kWarps) {
-    constexpr int P = D / 64;   // pairs per lane
-    const int t0 = lane * P;
     float a[P], bb[P];
     if (h < G) {
       const __nv_bfloat16* src = p.q + ((size_t)b * p.cache.hq + (size_t)G * g + h) * D;
+      uint32_t x[P / 2], y[P / 2];
+      if (P == 8) {
+        *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(src + t0);
+        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(src + D / 2 + t0);
+      } else {
+        *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(src + t0);
+        *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(src + D / 2 + t0);
+      }
 #pragma unroll
       for (int i = 0; i < P; i += 2) {
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(src + t0 + i);
-        const uint32_t y = *reinterpret_cast<const uint32_t*>(src + D / 2 + t0 + i);
-        a[i] = bf16_lo(x);
-        a[i + 1] = bf16_hi(x);
-        bb[i] = bf16_lo(y);
-        bb[i + 1] = bf16_hi(y);
+        a[i] = bf16_lo(x[i / 2]);
+        a[i + 1] = bf16_hi(x[i / 2]);
+        bb[i] = bf16_lo(y[i / 2]);
+        bb[i + 1] = bf16_hi(y[i / 2]);
       }
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        if (t0 < Blk::R) rope_pair(a[i], bb[i], rope_cs(p.tb, t0 + i, rope_pos));
+        if (t0 < Blk::R) rope_pair(a[i], bb[i], cs[i]);
         a[i] = round_bf16(a[i]);   // declared cast: roped q in bf16
         bb[i] = round_bf16(bb[i]);
       }
@@ -217,11 +228,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     const float down = __uint_as_float((uint32_t)(268 - eb) << 23);   // 2^(141 - eb)
     if (lane == 0) q_scale[h] = __uint_as_float((uint32_t)(eb - 14) << 23);   // 2^(eb - 141)
     float sum = 0.f;   // a lane's columns are all plain or all turned
+    uint32_t frag[2][P / 4][2];   // per half of the head and group of four columns: {0, 2} and {1, 3}
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      a[i] *= down;
-      bb[i] *= down;
-      sum += __half2float(__float2half_rn(a[i])) + __half2float(__float2half_rn(bb[i]));
+    for (int i = 0; i < P; i += 4) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        frag[0][i / 4][e] = pack_f16(a[i + e] * down, a[i + e + 2] * down);
+        frag[1][i / 4][e] = pack_f16(bb[i + e] * down, bb[i + e + 2] * down);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&frag[half][i / 4][e]));
+          sum += f.x + f.y;
+        }
+      }
     }
     const bool turned = GLOBAL && t0 < Blk::R;
     float plain_sum = turned ? 0.f : sum, turned_sum = turned ? sum : 0.f;
@@ -235,15 +254,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
       q_sum[1][h] = 128.0f * turned_sum;
     }
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int d = t0 + i + half * (D / 2);
-        const int dd = d & 63, cc = dd >> 4, t = (dd >> 2) & 3, e = dd & 3;
-        uint8_t* dst = q_s + ((half_of<GLOBAL>(d) * 2 + (t >> 1)) * 32 + h * 4 + cc) * 16 + (t & 1) * 8 + (e & 1) * 4 +
-                       (e >> 1) * 2;
-        *reinterpret_cast<__half*>(dst) = __float2half_rn(half ? bb[i] : a[i]);
-      }
+    for (int half = 0; half < 2; ++half) {   // a lane's columns are one group of four, or the two of a step pair
+      const int d = t0 + half * (D / 2), cc = (d & 63) >> 4, t = (d >> 2) & 3;
+      uint8_t* dst = q_s + ((half_of<GLOBAL>(d) * 2 + (t >> 1)) * 32 + h * 4 + cc) * 16 + (t & 1) * 8;
+      if (P == 8)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(frag[half][0][0], frag[half][0][1], frag[half][P / 4 - 1][0],
+                                                    frag[half][P / 4 - 1][1]);
+      else
+        *reinterpret_cast<uint2*>(dst) = make_uint2(frag[half][0][0], frag[half][0][1]);
     }
   }
   __syncthreads();
@@ -407,33 +425,57 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     }
   }
   __syncthreads();   // every stage has been read: reuse the ring for the warp merge
-  float* red_o = reinterpret_cast<float*>(smem);   // [warps][kHeads][D]
+  // The warps' outputs in fragment order ([warp][row tile][lane][4]: 16 bytes a lane, no bank conflicts);
+  // on sliding layers only lanes with heads (cq = 0) hold any.
+  constexpr int kTiles = S::kSegs * 8, kLanes = GLOBAL ? 32 : 8;
+  float4* red_o = reinterpret_cast<float4*>(smem);
+  const int my = GLOBAL ? lane : gq;
+  if (GLOBAL || cq == 0) {
 #pragma unroll
-  for (int i = 0; i < S::kSegs * 8; ++i) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int d = (i >> 3) * 128 + gq * 16 + 2 * (i & 7) + (r >> 1), h = 2 * cq + (r & 1);
-      if (h < S::kHeads) red_o[(warp * S::kHeads + h) * D + d] = (o[i][r] - ow[r & 1]) * kUp;
-    }
+    for (int i = 0; i < kTiles; ++i)
+      red_o[(warp * kTiles + i) * kLanes + my] = make_float4((o[i][0] - ow[0]) * kUp, (o[i][1] - ow[1]) * kUp,
+                                                             (o[i][2] - ow[0]) * kUp, (o[i][3] - ow[1]) * kUp);
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
-    const int h = i / D, d = i % D;
+  if (threadIdx.x < 8) {   // per head: the chunk's max and sum, and each warp's factor (a product of two: it may lie below 2^-126)
+    const int h = threadIdx.x;
     float M = red_m[0][h];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) M = fmaxf(M, red_m[w][h]);
-    float L = 0.f, O = 0.f;
+    float L = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       L = fmaf(red_l[w][h], ex2(red_m[w][h] - M), L);
-      const float f = ex2(0.5f * (red_m2[w][h] - kShift - M));   // its square may lie below 2^-126
-      O = fmaf(red_o[(w * S::kHeads + h) * D + d] * f, f, O);
+      factor[w][h] = ex2(0.5f * (red_m2[w][h] - kShift - M));
     }
-    const size_t s = slot + (size_t)h * p.NC;
-    p.ws_o[s * D + d] = O;
-    if (d == 0) {
-      p.ws_ml[s * 2 + 0] = L == 0.f ? -INFINITY : M;
-      p.ws_ml[s * 2 + 1] = L;
+    if (h < G) *reinterpret_cast<float2*>(p.ws_ml + (slot + (size_t)h * p.NC) * 2) = make_float2(L == 0.f ? -INFINITY : M, L);
+  }
+  __syncthreads();
+  // A thread merges, in warp order, four neighbouring row tiles of one lane: eight columns of two heads.
+  for (int i = threadIdx.x; i < S::kSegs * 2 * kLanes; i += kWarps * 32) {
+    const int ln = i % kLanes, t4 = i / kLanes;
+    const int lq = GLOBAL ? ln >> 2 : ln, lc = GLOBAL ? ln & 3 : 0;
+    float acc[2][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[0][e] = acc[1][e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f0 = factor[w][2 * lc], f1 = factor[w][2 * lc + 1];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float4 v = red_o[(w * kTiles + t4 * 4 + u) * kLanes + ln];
+        acc[0][2 * u] = fmaf(v.x * f0, f0, acc[0][2 * u]);
+        acc[1][2 * u] = fmaf(v.y * f1, f1, acc[1][2 * u]);
+        acc[0][2 * u + 1] = fmaf(v.z * f0, f0, acc[0][2 * u + 1]);
+        acc[1][2 * u + 1] = fmaf(v.w * f1, f1, acc[1][2 * u + 1]);
+      }
+    }
+    const int d = (t4 >> 1) * 128 + lq * 16 + (t4 & 1) * 8;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (2 * lc + j >= G) continue;
+      float* dst = p.ws_o + (slot + (size_t)(2 * lc + j) * p.NC) * D + d;
+      *reinterpret_cast<float4*>(dst) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+      *reinterpret_cast<float4*>(dst + 4) = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
     }
   }
 }
