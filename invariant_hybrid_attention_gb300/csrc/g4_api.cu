@@ -550,14 +550,9 @@ g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms
   if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
   const cudaStream_t cs = (cudaStream_t)stream;
   const PagedCache8 c8 = paged8(layer, cache, page_table, max_pages);
-  const void* q_eff = q;   // normed queries go through `out`, as in g4attn_decode_normed
-  if (nm.wq != nullptr || (global && nm.wk != nullptr)) {
-    if (launch_norm_queries(global, q, out, B, layer->n_q_heads, nm, cs) != cudaSuccess) return G4_ERR_CUDA;
-    q_eff = out;
-  }
   if (k_new && launch_kv8_append_decode(global, k_new, v_new, seq_len, pos, B, c8, nm, st, cs) != cudaSuccess)
     return G4_ERR_CUDA;
-  return from_cuda(launch_kv8_decode(global, q_eff, seq_len, pos, B, window, scale_log2(layer), c8, page_weights, out,
+  return from_cuda(launch_kv8_decode(global, q, seq_len, pos, B, window, scale_log2(layer), c8, nm, page_weights, out,
                                      workspace, st, cs));
 }
 

@@ -147,8 +147,8 @@ cudaError_t launch_kv8_unpack(bool global, const Kv8Range& range, const PagedCac
 size_t kv8_decode_workspace_bytes(bool global, int B, int max_pages, int window, int hq, int hkv, bool pages);
 // Decode partials, ordered merge and (page_weights set) the accumulated page weights.
 cudaError_t launch_kv8_decode(bool global, const void* q, const int32_t* seq_len, const int32_t* pos, int B, int window,
-                              float scale_log2, const PagedCache8& cache, float* page_weights, void* out, void* ws,
-                              const DeviceState& st, cudaStream_t s);
+                              float scale_log2, const PagedCache8& cache, const NormArgs& nm, float* page_weights,
+                              void* out, void* ws, const DeviceState& st, cudaStream_t s);
 cudaError_t launch_evict_pages(const int32_t* seq_len, const int32_t* table, const float* weights, int B, int max_pages,
                                int keep, int first, int last, int32_t* out_len, int32_t* out_table, float* out_weights,
                                int32_t* freed, int32_t* n_freed, const DeviceState& st, cudaStream_t s);

@@ -14,10 +14,18 @@ struct Vec {
   float a[8], b[8];   // columns t0 + i and D/2 + t0 + i
 };
 
+struct Raw {   // a lane's columns as bf16, as loaded
+  uint4 lo, hi;
+};
+
 template <int D>
-G4_DEV Vec<D> load_vec(const __nv_bfloat16* __restrict__ src, int t0) {
-  const uint4 lo = *reinterpret_cast<const uint4*>(src + t0);
-  const uint4 hi = *reinterpret_cast<const uint4*>(src + D / 2 + t0);
+G4_DEV Raw load_raw(const __nv_bfloat16* __restrict__ src, int t0) {
+  return Raw{*reinterpret_cast<const uint4*>(src + t0), *reinterpret_cast<const uint4*>(src + D / 2 + t0)};
+}
+
+template <int D>
+G4_DEV Vec<D> widen(const Raw& raw) {
+  const uint4 lo = raw.lo, hi = raw.hi;
   const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
   Vec<D> v;
 #pragma unroll
@@ -51,7 +59,7 @@ G4_DEV float unit_norm(Vec<D>& v, float eps) {
 
 template <int D>
 G4_DEV void weight(Vec<D>& v, const __nv_bfloat16* __restrict__ w, int t0) {
-  const Vec<D> m = load_vec<D>(w, t0);
+  const Vec<D> m = widen<D>(load_raw<D>(w, t0));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     v.a[i] *= m.a[i];
@@ -118,12 +126,33 @@ template <bool GLOBAL, bool NORM, int MODE>
 __global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs p) {
   using Blk = Kv8Block<GLOBAL>;
   constexpr int D = Blk::D, R = Blk::R, LPV = D / 16;
+  wait_for_grid();
+  let_next_grid_start();
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int n_rows = MODE == 0 ? p.rows.T : p.rows.B;
   const long long r64 = unit / p.parts;
   if (r64 >= n_rows) return;
   const int r = (int)r64, part = (int)(unit % p.parts);
+
+  const int HKV = p.cache.hkv, per = HKV / p.parts, g_lo = part * per, g_hi = g_lo + per;
+  const int t0 = (lane % LPV) * 8;       // this lane's pairs t0 .. t0 + 7
+  const int tr = (lane % (R / 8)) * 8;   // and its turning ones (sliding: the same)
+  const __nv_bfloat16* k_row = p.k + (size_t)r * HKV * D;
+  const __nv_bfloat16* v_row = GLOBAL ? nullptr : p.v + (size_t)r * HKV * D;
+  // The row's loads are in flight while its sequence, page and angles are looked up: all of a global
+  // row's (four heads at most, and the turned columns again, 8 lanes a head), the first two heads' of a
+  // sliding one, whose others follow two heads ahead.
+  Raw raw[4], raw_turned, raw_v;
+  if (GLOBAL) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < per) raw[i] = load_raw<D>(k_row + (size_t)(g_lo + i) * D, t0);
+    if ((lane >> 3) < per) raw_turned = load_raw<D>(k_row + (size_t)(g_lo + (lane >> 3)) * D, tr);
+  } else {
+    raw[0] = load_raw<D>(k_row + (size_t)(g_lo + lane / LPV) * D, t0);
+    raw_v = load_raw<D>(v_row + (size_t)(g_lo + lane / LPV) * D, t0);
+  }
 
   int b = r, idx, pos;   // sequence, held index and RoPE position of the row's token
   if (MODE == 0) {
@@ -161,10 +190,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs p) {
     return;
   }
   const int j = idx & 15;
-  const int HKV = p.cache.hkv, per = HKV / p.parts, g_lo = part * per, g_hi = g_lo + per;
   uint8_t* page = p.cache.pages + (size_t)phys * HKV * Blk::kBytes;
-  const __nv_bfloat16* k_row = p.k + (size_t)r * HKV * D;
-  const int tr = (lane % (R / 8)) * 8;   // this lane's turning pairs tr .. tr + 7
   float2 cs[8];
   {
     const float4* cx = p.tb.coarse_x + (size_t)(pos >> 8) * R + tr;
@@ -172,21 +198,20 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) cs[i] = rope_cs_exact(__ldg(cx + i), __ldg(fx + i));
   }
+  const uint32_t off_a = kv8_offset(j, t0), off_b = kv8_offset(j, D / 2 + t0);
   if (GLOBAL) {
-    const int t0 = lane * 8;
-    const uint32_t off_a = kv8_offset(j, t0), off_b = kv8_offset(j, D / 2 + t0);
-    float inv[4] = {1.f, 1.f, 1.f, 1.f};   // 1 / norm of each head (a full layer has four)
+    float inv[4] = {1.f, 1.f, 1.f, 1.f};   // 1 / norm of each head
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i >= per) break;
-      Vec<D> k = load_vec<D>(k_row + (size_t)(g_lo + i) * D, t0);
+      Vec<D> k = widen<D>(raw[i]);
       if (NORM && p.nm.v_norm) inv[i] = unit_norm<D>(k, p.nm.eps);
       uint8_t* blk = page + (size_t)(g_lo + i) * Blk::kBytes;
       store_vec<D>(blk, off_a, off_b, blk + Blk::kExp0 + j, k, lane == 0, 0xffffffffu);
     }
     const int i = lane >> 3;   // the turned columns of head g_lo + i
     if (i < per) {
-      Vec<D> k = load_vec<D>(k_row + (size_t)(g_lo + i) * D, tr);
+      Vec<D> k = widen<D>(raw_turned);
       if (NORM) {
         if (p.nm.v_norm) {
           const float s = i == 0 ? inv[0] : i == 1 ? inv[1] : i == 2 ? inv[2] : inv[3];
@@ -205,15 +230,16 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs p) {
                    0xffu << (lane & 24));
     }
   } else {
-    const int t0 = (lane % LPV) * 8;   // == tr
-    const uint32_t off_a = kv8_offset(j, t0), off_b = kv8_offset(j, D / 2 + t0);
     const unsigned mask = 0xffffu << (lane & 16);
-    const __nv_bfloat16* v_row = p.v + (size_t)r * HKV * D;
-#pragma unroll 2
+#pragma unroll 1
     for (int g0 = g_lo; g0 < g_hi; g0 += 2) {
       const int g = g0 + lane / LPV;
       uint8_t* blk = page + (size_t)g * Blk::kBytes;
-      Vec<D> k = load_vec<D>(k_row + (size_t)g * D, t0), v = load_vec<D>(v_row + (size_t)g * D, t0);
+      Vec<D> k = widen<D>(raw[0]), v = widen<D>(raw_v);
+      if (g0 + 2 < g_hi) {
+        raw[0] = load_raw<D>(k_row + (size_t)(g + 2) * D, t0);
+        raw_v = load_raw<D>(v_row + (size_t)(g + 2) * D, t0);
+      }
       if (NORM && p.nm.wk) {
         unit_norm<D>(k, p.nm.eps);
         weight<D>(k, p.nm.wk, t0);
@@ -283,6 +309,8 @@ template <bool GLOBAL>
 __global__ void __launch_bounds__(256) kv8_unpack_kernel(const UnpackArgs p) {
   using Blk = Kv8Block<GLOBAL>;
   constexpr int D = Blk::D;
+  wait_for_grid();
+  let_next_grid_start();
   const int lane = threadIdx.x & 31;
   const int HKV = p.src.hkv;
   const long long stride = (long long)gridDim.x * 8;
@@ -402,6 +430,8 @@ struct EvictArgs {
 template <int ITEMS>
 __global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
   __shared__ int counts[2][32];
+  wait_for_grid();
+  let_next_grid_start();
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
   const size_t row = (size_t)b * p.max_pages;
   const int base = warp * ITEMS * 32 + lane;
@@ -436,7 +466,7 @@ __global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
     const int at = base + 32 * i;
     key[i] = at >= e0 && at < e1 ? ordered_bits(w[i]) : 0xffffffffu;
   }
-  uint32_t T = 0;     // the largest value with fewer than drop (+ 1) keys below it: the drop-th smallest key
+  uint32_t T = 0;     // at last the drop-th smallest key, or any value with exactly drop keys below it
   int below = 0;      // keys below T
   int round = 0;
   if (drop > 0) {
@@ -446,10 +476,11 @@ __global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) x += key[i] < c ? 1 : 0;
       x = block_sum(__reduce_add_sync(0xffffffffu, x), round);
-      if (x < drop) {
+      if (x <= drop) {
         T = c;
         below = x;
       }
+      if (x == drop) break;   // exactly the pages below T leave
     }
   }
   const int ties = drop - below;   // pages of weight T that leave
@@ -514,10 +545,8 @@ cudaError_t append(AppendArgs& a, int n_rows, cudaStream_t s) {
   const long long blocks = ((long long)n_rows * a.parts + 7) / 8;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (a.nm.any())
-    kv8_append_kernel<GLOBAL, true, MODE><<<(unsigned)blocks, 256, 0, s>>>(a);
-  else
-    kv8_append_kernel<GLOBAL, false, MODE><<<(unsigned)blocks, 256, 0, s>>>(a);
-  return cudaGetLastError();
+    return launch_early(kv8_append_kernel<GLOBAL, true, MODE>, (unsigned)blocks, 256, 0, s, a);
+  return launch_early(kv8_append_kernel<GLOBAL, false, MODE>, (unsigned)blocks, 256, 0, s, a);
 }
 
 }  // namespace
@@ -546,11 +575,8 @@ cudaError_t launch_kv8_unpack(bool global, const Kv8Range& range, const PagedCac
   UnpackArgs a{range, src, dst, st.err};
   const long long units = (long long)range.rows.B * src.max_pages * src.hkv;   // at most
   const unsigned blocks = (unsigned)(units + 7 < 8LL * 152 * 8 ? (units + 7) / 8 : 152 * 8);
-  if (global)
-    kv8_unpack_kernel<true><<<blocks, 256, 0, s>>>(a);
-  else
-    kv8_unpack_kernel<false><<<blocks, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return global ? launch_early(kv8_unpack_kernel<true>, blocks, 256, 0, s, a)
+                : launch_early(kv8_unpack_kernel<false>, blocks, 256, 0, s, a);
 }
 
 cudaError_t launch_evict_pages(const int32_t* seq_len, const int32_t* table, const float* weights, int B, int max_pages,
@@ -561,13 +587,10 @@ cudaError_t launch_evict_pages(const int32_t* seq_len, const int32_t* table, con
   // Few pages per thread while that keeps the block small (its barriers are what a short row costs).
   const int items = max_pages <= 1024 ? 2 : max_pages <= 4096 ? 4 : 16;
   const unsigned threads = (unsigned)((max_pages + 32 * items - 1) / (32 * items) * 32);
-  if (items == 2)
-    evict_pages_kernel<2><<<B, threads, 0, s>>>(a);
-  else if (items == 4)
-    evict_pages_kernel<4><<<B, threads, 0, s>>>(a);
-  else
-    evict_pages_kernel<16><<<B, threads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(items == 2   ? evict_pages_kernel<2>
+                      : items == 4 ? evict_pages_kernel<4>
+                                   : evict_pages_kernel<16>,
+                      (unsigned)B, threads, 0, s, a);
 }
 
 }  // namespace g4

@@ -77,6 +77,28 @@ G4_DEV uint2 kv8_codes(const float (&x)[8], uint32_t biased) {
   return make_uint2(w[0], w[1]);
 }
 
+// Programmatic dependent launch. Every kernel of the 8-bit cache waits for the grid before it at its
+// first instruction (its end and its writes), and then lets the next grid of the stream start: back to
+// back, the launch of one hides behind the other, and nothing is read early.
+G4_DEV void wait_for_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+G4_DEV void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t s,
+                         const Args&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // Paged 8-bit cache of one layer, and the head counts of the call.
 struct PagedCache8 {
   uint8_t* pages;

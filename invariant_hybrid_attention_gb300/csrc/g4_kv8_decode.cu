@@ -57,6 +57,7 @@ struct Decode8Params {
   int window;
   float scale_log2;
   PagedCache8 cache;
+  NormArgs nm;          // query norm, and the key norm's weight on a global layer's plain columns
   float* ws_ml;         // [B][hq][NC][2]: running max (log2 units) and sum
   float* ws_o;          // [B][hq][NC][D]: un-normalised output, relative to that max
   float* ws_page;       // [B][hkv][max_pages][8]: log2 of each page's weight, or NULL
@@ -92,11 +93,6 @@ G4_DEV uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Programmatic dependent launch: lets the next kernel of the stream start its blocks; waits for the
-// kernel before this one to finish and its writes to be visible.
-G4_DEV void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-G4_DEV void wait_for_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Position checks shared by the two kernels: the held index of request b's token, or -1.
 G4_DEV int held_index(const int32_t* seq_len, const int32_t* pos, int b, int max_pages, int& rope_pos) {
   const int idx = seq_len[b] - 1;
@@ -112,6 +108,36 @@ G4_DEV int half_of(int d) {
   return sh == 0 ? 6 : sh == 4 ? 7 : sh < 4 ? sh - 1 : sh - 2;
 }
 
+// The norm of a query head held by a warp (lane: columns t0 .. and D/2 + t0 ..), times its weight; on a
+// global layer's plain columns also the key norm's weight, which the stored S lacks. The result is cast
+// to bf16 (a declared cast), as in the bf16 decode.
+template <bool GLOBAL>
+G4_DEV void norm_query(const NormArgs& nm, int t0, float (&a)[Shape<GLOBAL>::D / 64], float (&b)[Shape<GLOBAL>::D / 64]) {
+  constexpr int D = Shape<GLOBAL>::D, P = D / 64;
+  if (nm.wq) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, w);
+    const float inv = __frsqrt_rn(fmaf(ss, 1.0f / (float)D, nm.eps));
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      a[i] = (a[i] * inv) * bf16_to_f(nm.wq[t0 + i]);
+      b[i] = (b[i] * inv) * bf16_to_f(nm.wq[D / 2 + t0 + i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    if (GLOBAL && nm.wk && t0 >= Shape<GLOBAL>::Blk::R) {
+      a[i] *= bf16_to_f(nm.wk[t0 + i]);
+      b[i] *= bf16_to_f(nm.wk[D / 2 + t0 + i]);
+    }
+    a[i] = round_bf16(a[i]);
+    b[i] = round_bf16(b[i]);
+  }
+}
+
 template <bool GLOBAL, bool PAGES>
 __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode8Params p) {
   using S = Shape<GLOBAL>;
@@ -124,6 +150,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   __shared__ float q_scale[8], q_sum[2][8];   // per head: power of two, 128 x sum of q over the plain and turned columns
   __shared__ float red_m[kWarps][8], red_l[kWarps][8], red_m2[kWarps][8], factor[kWarps][8];
 
+  wait_for_grid();
   let_next_grid_start();
   const int HKV = p.cache.hkv, G = p.cache.hq / HKV;
   const int cr = blockIdx.x % p.NC;                    // chunk slot, KV head, request
@@ -208,6 +235,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
         bb[i] = bf16_lo(y[i / 2]);
         bb[i + 1] = bf16_hi(y[i / 2]);
       }
+      if (p.nm.wq || (GLOBAL && p.nm.wk)) norm_query<GLOBAL>(p.nm, t0, a, bb);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         if (t0 < Blk::R) rope_pair(a[i], bb[i], cs[i]);
@@ -487,112 +515,146 @@ G4_DEV int chunks_of(int last, int window, int chunk) {
 }
 
 // ---- ordered merge of the chunks, and the accumulated page weights -----------------------------------------
-// Blocks [0, merge_blocks) merge: one per (request, head, 128 columns). Chunk c's weight 2^(m_c - M) is
-// computed once, by lane c % 32; warp w then adds the chunks c = w (mod 4) in ascending order, eight
-// loads in flight, and the four sums are added in warp order: a tree fixed by the chunk numbers. A
-// refused request gets zeros. The other blocks add page_weights[b][i] += sum over heads of the page's
-// share of the softmax, a thread per page, heads in ascending order.
-// The kernel starts while the last chunk blocks run and waits for them before its first read
-// (programmatic dependent launch): its launch and the position look-ups cost no time of their own.
+// Merge units are (request, head, 128 columns). The chunks c = q (mod 4) of a unit are added in ascending
+// order, q = 0 .. 3, and the four sums in the order of q: a tree fixed by the chunk numbers. With SPLIT 1 a
+// warp does a unit, sixteen loads in flight; with SPLIT 4 (long page tables: few units of many chunks)
+// the four warps of a block take one sum each. A refused request gets zeros. The blocks after them add
+// page_weights[b][i] += sum over heads of the page's share of the softmax, a thread per page, heads in
+// ascending order.
 constexpr int kFinishThreads = 128;
 
-template <int D, bool PAGES>
-__global__ void __launch_bounds__(kFinishThreads) kv8_finish_kernel(const Decode8Params p, int chunk, unsigned merge_blocks,
-                                                                    int blocks_per_row, __nv_bfloat16* out,
-                                                                    float* page_weights) {
+template <int D, bool PAGES, int SPLIT>
+__global__ void __launch_bounds__(kFinishThreads) kv8_finish_kernel(const Decode8Params p, int chunk, unsigned units,
+                                                                    unsigned merge_blocks, int blocks_per_row,
+                                                                    __nv_bfloat16* out, float* page_weights) {
+  wait_for_grid();
+  let_next_grid_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hq = p.cache.hq;
   if (!PAGES || blockIdx.x < merge_blocks) {
     __shared__ float4 part[3][32];
     constexpr int kCols = D / 128;
-    const int col = (blockIdx.x % kCols) * 128 + lane * 4;
-    const int h = (blockIdx.x / kCols) % hq, b = blockIdx.x / kCols / hq;
+    const unsigned unit = SPLIT == 4 ? blockIdx.x : blockIdx.x * 4 + warp;
+    if (unit >= units) return;
+    const int col = (unit % kCols) * 128 + lane * 4;
+    const int h = (unit / kCols) % hq, b = unit / kCols / hq;
     int rope_pos;
     const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
     const int n = last < 0 ? 0 : min(p.NC, chunks_of(last, p.window, chunk));
     const size_t s0 = ((size_t)b * hq + h) * p.NC;
-    wait_for_grid();
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + s0;
-    float M = -INFINITY;
-    for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[c].x);
+    const float* o_src = p.ws_o + s0 * D + col;
+    const float2 none = make_float2(-INFINITY, 0.f);
+    float2 v = lane < n ? ml[lane] : none;   // lane l: chunk l, later 32 k + l
+    float M = v.x;
+#pragma unroll 4
+    for (int c = 32 + lane; c < n; c += 32) M = fmaxf(M, ml[c].x);
 #pragma unroll
     for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
     float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int c0 = 0; c0 < n; c0 += 32) {
-      const float2 v = c0 + lane < n ? ml[c0 + lane] : make_float2(-INFINITY, 0.f);
+      const float2 next = c0 + 32 + lane < n ? ml[c0 + 32 + lane] : none;
       const bool some = v.x != -INFINITY;   // a chunk that added nothing did not write its output slot
       const float wc = some ? ex2(v.x - M) : 0.f;
       if (some) L = fmaf(v.y, wc, L);
+      v = next;
       const unsigned wrote = __ballot_sync(0xffffffffu, some);
-      float4 o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = warp + 4 * i;
-        o[i] = ((wrote >> c) & 1u) ? *reinterpret_cast<const float4*>(p.ws_o + (s0 + c0 + c) * D + col)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      for (int half = 0; half < (SPLIT == 4 ? 1 : 2); ++half) {
+        constexpr int kLoads = SPLIT == 4 ? 8 : 16;
+        if (SPLIT == 1 && c0 + 16 * half >= n) break;
+        float4 o[kLoads];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = __shfl_sync(0xffffffffu, wc, warp + 4 * i);
-        acc.x = fmaf(o[i].x, w, acc.x);
-        acc.y = fmaf(o[i].y, w, acc.y);
-        acc.z = fmaf(o[i].z, w, acc.z);
-        acc.w = fmaf(o[i].w, w, acc.w);
+        for (int i = 0; i < kLoads; ++i) {
+          const int c = SPLIT == 4 ? warp + 4 * i : 16 * half + i;
+          o[i] = ((wrote >> c) & 1u) ? *reinterpret_cast<const float4*>(o_src + (size_t)(c0 + c) * D)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const float w = __shfl_sync(0xffffffffu, wc, SPLIT == 4 ? warp + 4 * i : 16 * half + i);
+          float4& s = acc[SPLIT == 4 ? 0 : i & 3];
+          s.x = fmaf(o[i].x, w, s.x);
+          s.y = fmaf(o[i].y, w, s.y);
+          s.z = fmaf(o[i].z, w, s.z);
+          s.w = fmaf(o[i].w, w, s.w);
+        }
       }
     }
 #pragma unroll
     for (int w = 16; w >= 1; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
-    if (warp > 0) part[warp - 1][lane] = acc;
-    __syncthreads();
-    if (warp > 0) return;
+    if (SPLIT == 4) {
+      if (warp > 0) part[warp - 1][lane] = acc[0];
+      __syncthreads();
+      if (warp > 0) return;
 #pragma unroll
-    for (int w = 0; w < 3; ++w) {
-      const float4 q = part[w][lane];
-      acc.x += q.x;
-      acc.y += q.y;
-      acc.z += q.z;
-      acc.w += q.w;
+      for (int i = 1; i < 4; ++i) acc[i] = part[i - 1][lane];
+    }
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      acc[0].x += acc[i].x;
+      acc[0].y += acc[i].y;
+      acc[0].z += acc[i].z;
+      acc[0].w += acc[i].w;
     }
     const float inv = L == 0.f ? 0.f : __frcp_rn(L);
     uint2 pk;
-    pk.x = pack_bf16(acc.x * inv, acc.y * inv);
-    pk.y = pack_bf16(acc.z * inv, acc.w * inv);
+    pk.x = pack_bf16(acc[0].x * inv, acc[0].y * inv);
+    pk.y = pack_bf16(acc[0].z * inv, acc[0].w * inv);
     *reinterpret_cast<uint2*>(out + ((size_t)b * hq + h) * D + col) = pk;
     return;
   }
   __shared__ float ref[kSlidingHq];   // log2 of each head's softmax sum
   const int unit = blockIdx.x - merge_blocks;
-  const int b = unit / blocks_per_row, i0 = (unit % blocks_per_row) * kFinishThreads;
+  const int b = unit / blocks_per_row, i = (unit % blocks_per_row) * kFinishThreads + threadIdx.x;
   int rope_pos;
   const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
   const int n_pages = (last >> 4) + 1;   // 0 when refused
-  if (i0 >= n_pages) return;
+  if (i - (int)threadIdx.x >= n_pages) return;
   const int HKV = p.cache.hkv, G = hq / HKV;
   const int n = min(p.NC, chunks_of(last, 0, chunk));
-  wait_for_grid();
-  for (int h = warp; h < hq; h += kFinishThreads / 32) {
-    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)b * hq + h) * p.NC;
-    float M = -INFINITY;
-    for (int c = lane; c < n; c += 32) M = fmaxf(M, ml[c].x);
+  float4 x[2 * kGlobalHkv];   // this page's weights, in flight while the sums are formed
 #pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-    float L = 0.f;
-    if (M != -INFINITY)
-      for (int c = lane; c < n; c += 32) L = fmaf(ml[c].y, ex2(ml[c].x - M), L);
+  for (int g = 0; g < kGlobalHkv; ++g) {
+    if (g >= HKV || i >= n_pages) continue;
+    const float4* src = reinterpret_cast<const float4*>(p.ws_page + (((size_t)b * HKV + g) * p.cache.max_pages + i) * 8);
+    x[2 * g] = src[0];
+    x[2 * g + 1] = src[1];
+  }
+  {   // four threads a head, chunks q, q + 4, ... each, one pass with a running maximum
+    const int h = threadIdx.x >> 2, q = threadIdx.x & 3;
+    float M = kNone, L = 0.f;
+    if (h < hq) {
+      const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)b * hq + h) * p.NC;
+#pragma unroll 8
+      for (int c = q; c < n; c += 4) {
+        const float2 v = ml[c];
+        const float mn = fmaxf(M, v.x);
+        L = fmaf(L, ex2(M - mn), v.x == -INFINITY ? 0.f : v.y * ex2(v.x - mn));
+        M = mn;
+      }
+    }
 #pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
-    if (lane == 0) ref[h] = M == -INFINITY ? INFINITY : M + log2f(L);   // no key: every share is 0
+    for (int w = 1; w <= 2; w <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, M, w), l2 = __shfl_xor_sync(0xffffffffu, L, w);
+      const float mn = fmaxf(M, m2);
+      L = L * ex2(M - mn) + l2 * ex2(m2 - mn);
+      M = mn;
+    }
+    if (q == 0 && h < hq) ref[h] = L == 0.f ? INFINITY : M + log2f(L);   // no key: every share is 0
   }
   __syncthreads();
-  const int i = i0 + threadIdx.x;
   if (i >= n_pages) return;
   float sum = 0.f;
-#pragma unroll 4
-  for (int g = 0; g < HKV; ++g) {
-    const float4* src = reinterpret_cast<const float4*>(p.ws_page + (((size_t)b * HKV + g) * p.cache.max_pages + i) * 8);
-    const float4 x = src[0], y = src[1];
-    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int g = 0; g < kGlobalHkv; ++g) {
+    if (g >= HKV) break;
+    const float v[8] = {x[2 * g].x, x[2 * g].y, x[2 * g].z, x[2 * g].w, x[2 * g + 1].x, x[2 * g + 1].y, x[2 * g + 1].z,
+                        x[2 * g + 1].w};
 #pragma unroll
     for (int h = 0; h < 8; ++h)
       if (h < G) sum += ex2(v[h] - ref[G * g + h]);
@@ -612,21 +674,15 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int D, bool PAGES>
 cudaError_t finish(const Decode8Params& p, int chunk, void* out, float* page_weights, cudaStream_t s) {
-  const long long merge_blocks = (long long)p.B * p.cache.hq * (D / 128);
+  const long long units = (long long)p.B * p.cache.hq * (D / 128);
+  const bool split = p.NC > 32;   // one warp's sixteen loads at a time would be a long chain
+  const long long merge_blocks = split ? units : (units + 3) / 4;
   const int per_row = (p.cache.max_pages + kFinishThreads - 1) / kFinishThreads;
   const long long blocks = merge_blocks + (PAGES ? (long long)p.B * per_row : 0);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kFinishThreads);
-  cfg.stream = s;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_finish_kernel<D, PAGES>, p, chunk, (unsigned)merge_blocks, per_row,
-                            (__nv_bfloat16*)out, page_weights);
+  if (blocks > 0x7fffffffLL || units > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_early(split ? kv8_finish_kernel<D, PAGES, 4> : kv8_finish_kernel<D, PAGES, 1>, (unsigned)blocks,
+                      kFinishThreads, 0, s, p, chunk, (unsigned)units, (unsigned)merge_blocks, per_row,
+                      (__nv_bfloat16*)out, page_weights);
 }
 
 template <bool GLOBAL, bool PAGES>
@@ -644,8 +700,7 @@ cudaError_t launch(const Decode8Params& p, cudaStream_t s) {
   }
   const long long blocks = (long long)p.NC * p.cache.hkv * p.B;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  kv8_decode_kernel<GLOBAL, PAGES><<<(unsigned)blocks, kWarps * 32, Shape<GLOBAL>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_early(kv8_decode_kernel<GLOBAL, PAGES>, (unsigned)blocks, kWarps * 32, Shape<GLOBAL>::kSmem, s, p);
 }
 
 }  // namespace
@@ -659,8 +714,8 @@ size_t kv8_decode_workspace_bytes(bool global, int B, int max_pages, int window,
 }
 
 cudaError_t launch_kv8_decode(bool global, const void* q, const int32_t* seq_len, const int32_t* pos, int B, int window,
-                              float scale_log2, const PagedCache8& cache, float* page_weights, void* out, void* ws,
-                              const DeviceState& st, cudaStream_t s) {
+                              float scale_log2, const PagedCache8& cache, const NormArgs& nm, float* page_weights, void* out,
+                              void* ws, const DeviceState& st, cudaStream_t s) {
   if (B <= 0) return cudaSuccess;
   Decode8Params p{};
   p.q = (const __nv_bfloat16*)q;
@@ -670,6 +725,7 @@ cudaError_t launch_kv8_decode(bool global, const void* q, const int32_t* seq_len
   p.window = global ? 0 : window;
   p.scale_log2 = scale_log2;
   p.cache = cache;
+  p.nm = nm;
   p.NC = chunk_slots(global, cache.max_pages, window);
   const size_t D = global ? kGlobalD : kSlidingD;
   const size_t slots = (size_t)B * cache.hq * p.NC;
