@@ -123,9 +123,10 @@ G4_DEV bool rows_ok(const SeqRows& r, int qs, int L, int cs) {
 // arithmetic. Sliding: half a warp per vector, two heads at a time, K' and V together. Global: a warp
 // per head for S, then 8 lanes per head for the turned columns of up to four heads at once.
 template <bool GLOBAL, bool NORM, int MODE>
-__global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs p) {
+__global__ void __launch_bounds__(256, 3) kv8_append_kernel(const AppendArgs p) {
   using Blk = Kv8Block<GLOBAL>;
   constexpr int D = Blk::D, R = Blk::R, LPV = D / 16;
+  __shared__ __align__(16) float2 angles[8][R];
   wait_for_grid();
   let_next_grid_start();
   const int lane = threadIdx.x & 31;
@@ -191,12 +192,31 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs p) {
   }
   const int j = idx & 15;
   uint8_t* page = p.cache.pages + (size_t)phys * HKV * Blk::kBytes;
+  // The row's angles: pair t by lane t % 32 (whole lines of the tables), then to the lanes that turn by
+  // them through shared memory, two pairs to 16 bytes, [i / 2][lane] so that the reads conflict on no bank.
   float2 cs[8];
   {
-    const float4* cx = p.tb.coarse_x + (size_t)(pos >> 8) * R + tr;
-    const float4* fx = p.tb.fine_x + (size_t)(pos & 255) * R + tr;
+    const float4* cx = p.tb.coarse_x + (size_t)(pos >> 8) * R;
+    const float4* fx = p.tb.fine_x + (size_t)(pos & 255) * R;
+    float4 c4[R / 32], f4[R / 32];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = rope_cs_exact(__ldg(cx + i), __ldg(fx + i));
+    for (int k = 0; k < R / 32; ++k) {
+      c4[k] = __ldg(cx + 32 * k + lane);
+      f4[k] = __ldg(fx + 32 * k + lane);
+    }
+    float2* mine = angles[threadIdx.x >> 5];
+#pragma unroll
+    for (int k = 0; k < R / 32; ++k) {
+      const int t = 32 * k + lane;
+      mine[(((t & 7) >> 1) * (R / 8) + (t >> 3)) * 2 + (t & 1)] = rope_cs_exact(c4[k], f4[k]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(mine + (i * (R / 8) + (tr >> 3)) * 2);
+      cs[2 * i] = make_float2(v.x, v.y);
+      cs[2 * i + 1] = make_float2(v.z, v.w);
+    }
   }
   const uint32_t off_a = kv8_offset(j, t0), off_b = kv8_offset(j, D / 2 + t0);
   if (GLOBAL) {

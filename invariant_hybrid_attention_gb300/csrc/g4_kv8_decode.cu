@@ -28,6 +28,7 @@ namespace g4 {
 
 namespace {
 
+constexpr int kChunkSliding = kDecodeChunkSliding, kChunkGlobal = kDecodeChunkGlobal;   // keys per chunk
 constexpr int kWarps = 4;
 constexpr int kStages = 2;             // pages in flight per warp
 constexpr float kLazy = 8.0f;          // m2 moves when the maximum grows by more than 2^8
@@ -41,7 +42,7 @@ struct Shape {
   static constexpr int kSegs = D / 128;                  // 128-column segments of V
   static constexpr int kHalves = GLOBAL ? 8 : 4;         // 64-column halves of K: global 6 plain + 2 turned
   static constexpr int kHeads = GLOBAL ? 8 : 2;          // at most; columns beyond the group carry q = 0
-  static constexpr int kChunk = GLOBAL ? kDecodeChunkGlobal : kDecodeChunkSliding;
+  static constexpr int kChunk = GLOBAL ? kChunkGlobal : kChunkSliding;
   static constexpr int kStage = (Blk::kBytes + 127) / 128 * 128;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kQ = kHalves * 1024;              // q fragments: [half][2][32 lanes][16 bytes]
@@ -159,6 +160,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, cq = lane & 3;             // matrix fragment coordinates
 
+  const int32_t* table = p.cache.page_table + (size_t)b * p.cache.max_pages;
+  int phys = 0;
+  if (GLOBAL) {   // the chunk is known before the length: its table entries load along with it
+    const int i = cr * (S::kChunk / kPage) + warp + kWarps * lane;
+    if (lane < S::kChunk / kPage / kWarps && i < p.cache.max_pages) phys = table[i];
+  }
   int rope_pos;
   const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
   if (last < 0) {
@@ -171,27 +178,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   const int k_end = min(last, c * S::kChunk + S::kChunk - 1);   // inclusive
   if (k_begin > k_end) return;                                    // unused slot
 
-  // This warp's pages: warp, warp + 4, ... of the chunk's; lane n keeps the n-th one's physical page.
+  // This warp's pages: warp, warp + 4, ... of the chunk's; lane n keeps the n-th one's physical page. A
+  // warp that finds one outside the pool copies none of its pages, and the chunk then adds nothing.
   const int pg0 = k_begin >> 4, n_pages = (k_end >> 4) - pg0 + 1;
-  const int mine = n_pages > warp ? (n_pages - warp + kWarps - 1) / kWarps : 0;   // at most 16
-  int phys = 0;
-  if (lane < mine) phys = p.cache.page_table[(size_t)b * p.cache.max_pages + pg0 + warp + kWarps * lane];
-  const bool bad = lane < mine && (phys < 0 || phys >= p.cache.num_pages);
+  int mine = n_pages > warp ? (n_pages - warp + kWarps - 1) / kWarps : 0;   // at most 32
+  if (!GLOBAL && lane < mine) phys = table[pg0 + warp + kWarps * lane];
+  const bool bad = __any_sync(0xffffffffu, lane < mine && (phys < 0 || phys >= p.cache.num_pages));
+  if (bad) mine = 0;
   if (threadIdx.x == 0) abort_flag = 0;
-  if (lane < kStages) mbar_init(&full[warp][lane], 1);
+  if (lane < kStages) mbar_init(&full[warp][lane], 1);   // a warp's barriers are its own
   fence_mbar_init();
+  __syncwarp();
   const size_t slot = ((size_t)b * p.cache.hq + (size_t)G * g) * p.NC + cr;   // head G g + h adds h NC
-  if (__syncthreads_or(bad)) {   // a page outside the pool: this chunk adds nothing
-    if (threadIdx.x == 0) set_error(p.err, kErrPage);
-    if ((int)threadIdx.x < G) {
-      p.ws_ml[(slot + (size_t)threadIdx.x * p.NC) * 2 + 0] = -INFINITY;
-      p.ws_ml[(slot + (size_t)threadIdx.x * p.NC) * 2 + 1] = 0.f;
-    }
-    if (PAGES)
-      for (int i = threadIdx.x; i < n_pages * 8; i += kWarps * 32)
-        p.ws_page[(((size_t)b * HKV + g) * p.cache.max_pages + pg0) * 8 + i] = -INFINITY;
-    return;
-  }
 
   uint8_t* ring = smem + warp * kStages * S::kStage;
   auto issue = [&](int n, int page) {   // lane 0: copy this warp's n-th page
@@ -292,7 +290,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
         *reinterpret_cast<uint2*>(dst) = make_uint2(frag[half][0][0], frag[half][0][1]);
     }
   }
-  __syncthreads();
+  const bool void_chunk = __syncthreads_or(bad);
   const float qs[2] = {q_scale[2 * cq] * p.scale_log2, q_scale[2 * cq + 1] * p.scale_log2};
   const float q0[2] = {q_sum[0][2 * cq], q_sum[0][2 * cq + 1]}, q1[2] = {q_sum[1][2 * cq], q_sum[1][2 * cq + 1]};
 
@@ -453,6 +451,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     }
   }
   __syncthreads();   // every stage has been read: reuse the ring for the warp merge
+  if (void_chunk) {   // a page outside the pool: nothing but a state that adds nothing
+    if (threadIdx.x == 0) set_error(p.err, kErrPage);
+    if ((int)threadIdx.x < G)
+      *reinterpret_cast<float2*>(p.ws_ml + (slot + (size_t)threadIdx.x * p.NC) * 2) = make_float2(-INFINITY, 0.f);
+    if (PAGES)
+      for (int i = threadIdx.x; i < n_pages * 8; i += kWarps * 32)
+        p.ws_page[(((size_t)b * HKV + g) * p.cache.max_pages + pg0) * 8 + i] = -INFINITY;
+    return;
+  }
   // The warps' outputs in fragment order ([warp][row tile][lane][4]: 16 bytes a lane, no bank conflicts);
   // on sliding layers only lanes with heads (cq = 0) hold any.
   constexpr int kTiles = S::kSegs * 8, kLanes = GLOBAL ? 32 : 8;
@@ -664,9 +671,9 @@ __global__ void __launch_bounds__(kFinishThreads) kv8_finish_kernel(const Decode
 
 int chunk_slots(bool global, int max_pages, int window) {
   const long long keys = (long long)max_pages * kPage < kMaxPos ? (long long)max_pages * kPage : kMaxPos;
-  if (global) return (int)((keys + kDecodeChunkGlobal - 1) / kDecodeChunkGlobal);
-  const int by_window = (window - 1) / kDecodeChunkSliding + 2;
-  const int by_table = (int)((keys + kDecodeChunkSliding - 1) / kDecodeChunkSliding);
+  if (global) return (int)((keys + kChunkGlobal - 1) / kChunkGlobal);
+  const int by_window = (window - 1) / kChunkSliding + 2;
+  const int by_table = (int)((keys + kChunkSliding - 1) / kChunkSliding);
   return by_window < by_table ? by_window : by_table;
 }
 
@@ -744,9 +751,9 @@ cudaError_t launch_kv8_decode(bool global, const void* q, const int32_t* seq_len
   else
     e = page_weights ? launch<true, true>(p, s) : launch<true, false>(p, s);
   if (e != cudaSuccess) return e;
-  if (!global) return finish<kSlidingD, false>(p, kDecodeChunkSliding, out, nullptr, s);
-  return page_weights ? finish<kGlobalD, true>(p, kDecodeChunkGlobal, out, page_weights, s)
-                      : finish<kGlobalD, false>(p, kDecodeChunkGlobal, out, nullptr, s);
+  if (!global) return finish<kSlidingD, false>(p, kChunkSliding, out, nullptr, s);
+  return page_weights ? finish<kGlobalD, true>(p, kChunkGlobal, out, page_weights, s)
+                      : finish<kGlobalD, false>(p, kChunkGlobal, out, nullptr, s);
 }
 
 }  // namespace g4
