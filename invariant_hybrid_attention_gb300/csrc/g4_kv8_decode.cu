@@ -28,7 +28,7 @@ namespace g4 {
 
 namespace {
 
-constexpr int kChunkSliding = kDecodeChunkSliding, kChunkGlobal = kDecodeChunkGlobal;   // keys per chunk
+constexpr int kChunkSliding = 512, kChunkGlobal = kDecodeChunkGlobal;   // keys per chunk
 constexpr int kWarps = 4;
 constexpr int kStages = 2;             // pages in flight per warp
 constexpr float kLazy = 8.0f;          // m2 moves when the maximum grows by more than 2^8
@@ -160,6 +160,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, cq = lane & 3;             // matrix fragment coordinates
 
+  // This warp's query heads, warp and warp + 4, in flight while the length and the pages are looked up.
+  constexpr int P = D / 64;   // pairs per lane: columns t0 .. t0 + P - 1 and D / 2 + t0 ..
+  constexpr int kMine = (S::kHeads + kWarps - 1) / kWarps;
+  const int t0 = lane * P;
+  uint32_t q_lo[kMine][P / 2], q_hi[kMine][P / 2];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int h = warp + kWarps * i;
+    if (h >= G) continue;
+    const __nv_bfloat16* src = p.q + ((size_t)b * p.cache.hq + (size_t)G * g + h) * D + t0;
+    if (P == 8) {
+      *reinterpret_cast<uint4*>(q_lo[i]) = *reinterpret_cast<const uint4*>(src);
+      *reinterpret_cast<uint4*>(q_hi[i]) = *reinterpret_cast<const uint4*>(src + D / 2);
+    } else {
+      *reinterpret_cast<uint2*>(q_lo[i]) = *reinterpret_cast<const uint2*>(src);
+      *reinterpret_cast<uint2*>(q_hi[i]) = *reinterpret_cast<const uint2*>(src + D / 2);
+    }
+  }
   const int32_t* table = p.cache.page_table + (size_t)b * p.cache.max_pages;
   int phys = 0;
   if (GLOBAL) {   // the chunk is known before the length: its table entries load along with it
@@ -207,31 +225,29 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   // The query heads of this KV head, turned, cast to bf16, scaled by a power of two each and laid out
   // as matrix fragments: lane (head, cc) of half i and step t holds columns 16 cc + 4t + {0, 2} and
   // {1, 3} of the half. One warp per head.
-  constexpr int P = D / 64;   // pairs per lane
-  const int t0 = lane * P;
   float2 cs[P];               // (cos, sin) of this lane's pairs, the same for every head
   if (t0 < Blk::R) {
 #pragma unroll
     for (int i = 0; i < P; ++i) cs[i] = rope_cs_t(p.tb, Blk::R, t0 + i, rope_pos);
   }
-  for (int h = warp; h < 8; h += kWarps) {
+  // Columns of the product beyond the group carry q = 0.
+  for (int h = S::kHeads + warp; h < 8; h += kWarps) {   // (a sliding layer's six)
+    for (int i = lane; i < S::kHalves * 2 * 4; i += 32)
+      *reinterpret_cast<uint4*>(q_s + ((i >> 2) * 32 + h * 4 + (i & 3)) * 16) = make_uint4(0, 0, 0, 0);
+    if (lane == 0) q_scale[h] = q_sum[0][h] = q_sum[1][h] = 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int h = warp + kWarps * k;
+    if (h >= S::kHeads) continue;
     float a[P], bb[P];
     if (h < G) {
-      const __nv_bfloat16* src = p.q + ((size_t)b * p.cache.hq + (size_t)G * g + h) * D;
-      uint32_t x[P / 2], y[P / 2];
-      if (P == 8) {
-        *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(src + t0);
-        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(src + D / 2 + t0);
-      } else {
-        *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(src + t0);
-        *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(src + D / 2 + t0);
-      }
 #pragma unroll
       for (int i = 0; i < P; i += 2) {
-        a[i] = bf16_lo(x[i / 2]);
-        a[i + 1] = bf16_hi(x[i / 2]);
-        bb[i] = bf16_lo(y[i / 2]);
-        bb[i + 1] = bf16_hi(y[i / 2]);
+        a[i] = bf16_lo(q_lo[k][i / 2]);
+        a[i + 1] = bf16_hi(q_lo[k][i / 2]);
+        bb[i] = bf16_lo(q_hi[k][i / 2]);
+        bb[i + 1] = bf16_hi(q_hi[k][i / 2]);
       }
       if (p.nm.wq || (GLOBAL && p.nm.wk)) norm_query<GLOBAL>(p.nm, t0, a, bb);
 #pragma unroll
