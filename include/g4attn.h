@@ -422,8 +422,9 @@ g4_status g4attn_kv8_prefill(const g4attn_layer* layer, const g4attn_norms* norm
 size_t g4attn_kv8_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, int32_t max_pages,
                                          int32_t page_weights);
 
-/* One decode step over an 8-bit cache (no counterpart in the RFC): g4attn_decode_normed, with the same
- * fixed chunks and merge order, and three additions.
+/* One decode step over an 8-bit cache (no counterpart in the RFC): g4attn_decode_normed, with fixed
+ * chunks of its own (512 keys on sliding layers, 1024 on global ones, aligned to held key 0, merged by a
+ * tree fixed by the chunk numbers) and three additions.
  *   k_new, v_new   both may be NULL: the newest token is in the cache already (g4attn_kv8_append).
  *   pos            int32 [B], device, or NULL: the RoPE position of each request's newest token. NULL:
  *                  seq_len[b] - 1. A sequence that lost pages (g4attn_evict_pages) holds seq_len[b] keys,
@@ -434,7 +435,10 @@ size_t g4attn_kv8_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, i
  *                  page_weights[b][i] += the softmax weight of held page i's keys, summed over the
  *                  query heads (a step adds n_q_heads over a sequence's pages). Entries past the held
  *                  pages are not touched. Calls that share a buffer must be ordered.
- * The query is turned and cast to bf16; the softmax weights are cast to fp16 for the value product. */
+ * The query is turned and cast to bf16; the softmax weights are cast to fp16 for the value product. out may be
+ * q. Calls that may run at the same time need workspaces of their own; its contents on entry do not
+ * matter. A key that holds a NaN vector makes the rows of its head that see it NaN, and the page weights
+ * of their requests. */
 g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k_new,
                             const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B,
                             const g4attn_cache8* cache, const int32_t* page_table, int32_t max_pages,
@@ -448,7 +452,7 @@ g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms
  *   out_seq_len [B]             seq_len - 16 per evicted page
  *   out_table, out_weights [B][max_pages]  the kept pages and their weights, then -1 and 0
  *   freed [B][max_pages], n_freed [B]      the evicted physical pages in their order, then -1
- * out_seq_len, out_table and out_weights may be the inputs. max_pages <= 16384. All arrays are device
+ * out_seq_len, out_table and out_weights may be the inputs; freed and n_freed may not. max_pages <= 16384. All arrays are device
  * int32 (weights: float). A sequence whose seq_len is below 0, past 262144 or past the table is passed
  * on whole (its max_pages entries) and sets G4_ERR_DEVICE. */
 g4_status g4attn_evict_pages(const int32_t* seq_len, const int32_t* page_table, const float* page_weights, int32_t B,

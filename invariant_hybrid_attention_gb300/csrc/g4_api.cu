@@ -589,6 +589,7 @@ int32_t g4attn_provenance(const g4attn_layer* layer, char* buf, size_t len) {
                  "ktile128@abs-pos,ascending;split=decode-fixed-chunk-1024@abs-key0,4-warp-round-robin,ordered-merge;"
                  "qrope=attention-kernel(plain),append-pass(normed,vision,exact-decode);"
                  "exact-decode=prefill-kernels-one-row-chunks;vision=image-span-per-row;"
+                 "kv8=int8-pow2-step-per-token-head,split-1024@abs-key0,weights:fp16-rne;"
                  "accumulator=fp32;casts=roped-q,roped-k,p,out:bf16-rne;exp=ex2.approx.ftz.f32;device=%s;dtype=bf16;"
                  "shape=Hq%d,Hkv%d,D512,k_eq_v,prope0.25,theta1e6,scale%.9g;fallback=none",
                  dev, layer->n_q_heads, layer->n_kv_heads, (double)layer->softmax_scale);
@@ -600,6 +601,7 @@ int32_t g4attn_provenance(const g4attn_layer* layer, char* buf, size_t len) {
                  "split=decode-fixed-chunk-256@abs-key0,4-warp-round-robin,ordered-merge;"
                  "qrope=attention-kernel(plain),append-pass(normed,vision,exact-decode);"
                  "exact-decode=prefill-kernels-one-row-chunks;vision=image-span-per-row;"
+                 "kv8=int8-pow2-step-per-token-head,split-512@abs-key0,weights:fp16-rne;"
                  "accumulator=fp32;casts=roped-q,roped-k,p,out:bf16-rne;exp=ex2.approx.ftz.f32;device=%s;dtype=bf16;"
                  "shape=Hq%d,Hkv%d,D256,W%d,theta1e4,scale%.9g;fallback=none",
                  dev, layer->n_q_heads, layer->n_kv_heads, layer->window, (double)layer->softmax_scale);

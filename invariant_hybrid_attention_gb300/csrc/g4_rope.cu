@@ -103,9 +103,14 @@ cudaError_t device_state(DeviceState* st) {
   std::lock_guard<std::mutex> lock(g_state_mutex);
   if (!g_state_ready[dev]) {
     static HostTables hs, hg;
-    if (hs.coarse.empty()) {
-      build_tables(kSlidingD, kSlidingR, 1.0e4, hs);
-      build_tables(kGlobalD, kGlobalR, 1.0e6, hg);
+    try {   // no exception leaves a C entry point
+      if (hg.fine_x.empty()) {
+        build_tables(kSlidingD, kSlidingR, 1.0e4, hs);
+        build_tables(kGlobalD, kGlobalR, 1.0e6, hg);
+      }
+    } catch (...) {
+      hg.fine_x.clear();
+      return cudaErrorMemoryAllocation;
     }
     DeviceState s{};
     void* p = nullptr;
@@ -541,18 +546,20 @@ __global__ void __launch_bounds__(256) append_prefill_kernel(const __nv_bfloat16
   if (NORM) lane_weights<D>(nm.wk, wk);
   if (q_out != nullptr) {
     constexpr int VPW = 32 / (D / 16);
+    // Staging alone, the heads may be shared out over gridDim.y blocks (of whole warps' vectors).
+    const int h_lo = (int)blockIdx.y * (HQ / (int)gridDim.y), h_hi = h_lo + HQ / (int)gridDim.y;
     if (NORM) {
       float wq[16];
       lane_weights<D>(nm.wq, wq);
       const float* fold = (SHARED && nm.wk != nullptr) ? wk : nullptr;   // w_k on the un-rotated dims
 #pragma unroll 2
-      for (int h0 = 0; h0 < HQ; h0 += VPW) {
+      for (int h0 = h_lo; h0 < h_hi; h0 += VPW) {
         const size_t v = (size_t)r * HQ + h0 + lane / (D / 16);
         vec8_normed<D, R>(q + v * D, RowDst{q_out + v * D}, cs, nm.wq != nullptr, nm.eps, wq, fold, R);
       }
     } else {
 #pragma unroll 4
-      for (int h0 = 0; h0 < HQ; h0 += VPW) {
+      for (int h0 = h_lo; h0 < h_hi; h0 += VPW) {
         const size_t v = (size_t)r * HQ + h0 + lane / (D / 16);
         rope_vec8_cs<D, R>(q + v * D, RowDst{q_out + v * D}, cs);
       }
@@ -829,7 +836,10 @@ cudaError_t launch_append_prefill(bool global, const void* k, const void* v, con
 cudaError_t launch_stage_queries(bool global, const void* q, void* q_out, const SeqRows& rows, const PagedCache& cache,
                                  const DeviceState& st, cudaStream_t s, const NormArgs& nm) {
   if (rows.T <= 0 || rows.B <= 0) return cudaSuccess;
-  const unsigned blocks = (unsigned)((rows.T + 7) / 8);
+  // Few rows: their heads go to several warps, four heads each at least (a row's bits do not depend on it).
+  unsigned parts = 1;
+  while (parts * 8 <= (unsigned)cache.hq && (long long)rows.T * parts < 152 * 32) parts *= 2;
+  const dim3 blocks((unsigned)((rows.T + 7) / 8), parts);
   const __nv_bfloat16* qb = (const __nv_bfloat16*)q;
   __nv_bfloat16* qo = (__nv_bfloat16*)q_out;
   const __nv_bfloat16* none = nullptr;
