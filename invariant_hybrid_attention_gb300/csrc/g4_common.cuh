@@ -81,10 +81,6 @@ struct RopeTables {
   const float2* coarse_t; // [kRopeCoarse][R]
   const float2* mid_t;    // [kRopeMid][R]
   const float2* fine_t;   // [kRopeFine][R]
-  // Two-level tables in two fp32 parts (cos, sin, and what their rounding left), entry-major, for the
-  // append into 8-bit pages: coarse_x[c][t] of 256*c*f_t, fine_x[a][t] of a*f_t, 0 <= a < 256.
-  const float4* coarse_x;   // [kRopeCoarse][R]
-  const float4* fine_x;     // [256][R]
 };
 
 // ---- small helpers -------------------------------------------------------------------------
@@ -125,35 +121,6 @@ G4_DEV float2 rope_cs(const RopeTables& tb, int t, int pos) {
   const float2 m = __ldg(tb.mid + t * kRopeMid + ((pos >> 4) & 15));
   const float2 f = __ldg(tb.fine + t * kRopeFine + (pos & 15));
   return cmul(cmul(c, m), f);
-}
-
-// rope_cs from the entry-major tables (R pairs per entry; the same bits): for lanes that hold
-// consecutive pairs.
-G4_DEV float2 rope_cs_t(const RopeTables& tb, int R, int t, int pos) {
-  const float2 c = __ldg(tb.coarse_t + (size_t)(pos >> 8) * R + t);
-  const float2 m = __ldg(tb.mid_t + ((pos >> 4) & 15) * R + t);
-  const float2 f = __ldg(tb.fine_t + (pos & 15) * R + t);
-  return cmul(cmul(c, m), f);
-}
-
-// a b - c d and its kind in two fp32 parts: products exact through fma, the sum's error kept, one rounding
-// at the end.
-G4_DEV float dot2_exact(float ah, float al, float bh, float bl, float ch, float cl, float dh, float dl) {
-  const float p = ah * bh, pe = fmaf(ah, bh, -p);
-  const float q = ch * dh, qe = fmaf(ch, dh, -q);
-  const float s = p + q, z = s - p;
-  const float se = (p - (s - z)) + (q - z);
-  float low = fmaf(ah, bl, fmaf(al, bh, fmaf(ch, dl, fmaf(cl, dh, pe + qe))));
-  return s + (se + low);
-}
-
-// (cos, sin)(pos * f_t) rounded once to fp32 (nearly always to the nearest): the angle-addition formula
-// on the two-part tables. Where rope_cs carries the rounding of three table entries and two products
-// (a few 2^-24), this leaves 2^-25, so that a value next to a border between two codes falls on the
-// border's right side as often as with exactly rounded angles.
-G4_DEV float2 rope_cs_exact(float4 a, float4 b) {
-  return make_float2(dot2_exact(a.x, a.z, b.x, b.z, -a.y, -a.w, b.y, b.w),
-                     dot2_exact(a.y, a.w, b.x, b.z, a.x, a.z, b.y, b.w));
 }
 
 // 2^x on the multi-function unit (PTX ex2.approx.ftz.f32; 2^-inf = +0). Results below 2^-126

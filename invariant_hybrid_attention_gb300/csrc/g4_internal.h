@@ -78,11 +78,6 @@ cudaError_t launch_append_prefill(bool global, const void* k, const void* v, con
                                   const PagedCache& cache, const DeviceState& st, cudaStream_t s,
                                   const void* q = nullptr, void* q_out = nullptr, const NormArgs& nm = NormArgs{});
 
-// The rows' queries alone, staged into q_out as launch_append_prefill does (normed, turned, bf16); of the
-// cache only hq, hkv and max_pages are read.
-cudaError_t launch_stage_queries(bool global, const void* q, void* q_out, const SeqRows& rows, const PagedCache& cache,
-                                 const DeviceState& st, cudaStream_t s, const NormArgs& nm);
-
 cudaError_t launch_append_decode(bool global, const void* k_new, const void* v_new, const int32_t* seq_len,
                                  int B, const PagedCache& cache, const DeviceState& st, cudaStream_t s,
                                  const NormArgs& nm = NormArgs{});
@@ -129,28 +124,5 @@ struct PartialSet {
 };
 cudaError_t launch_merge_partials(const PartialSet& parts, const SeqRows& rows, int hq, void* out, const DeviceState& st,
                                   cudaStream_t s);
-
-// ---- the 8-bit paged cache (g4_kv8.cuh: layout and cast; g4_kv8.cu, g4_kv8_decode.cu) ---------------------
-struct PagedCache8;
-struct Kv8Range;
-
-// Writes the rows of a prefill batch into 8-bit pages.
-cudaError_t launch_kv8_append(bool global, const void* k, const void* v, const SeqRows& rows, const PagedCache8& cache,
-                              const NormArgs& nm, const DeviceState& st, cudaStream_t s);
-// Writes one new token per request at held index seq_len - 1, turned by pos (NULL: the held index).
-cudaError_t launch_kv8_append_decode(bool global, const void* k_new, const void* v_new, const int32_t* seq_len,
-                                     const int32_t* pos, int B, const PagedCache8& cache, const NormArgs& nm,
-                                     const DeviceState& st, cudaStream_t s);
-// Reads keys of 8-bit pages back into bf16 pages (dst.page_table: the destination's page table).
-cudaError_t launch_kv8_unpack(bool global, const Kv8Range& range, const PagedCache8& src, const PagedCache& dst,
-                              const DeviceState& st, cudaStream_t s);
-size_t kv8_decode_workspace_bytes(bool global, int B, int max_pages, int window, int hq, int hkv, bool pages);
-// Decode partials, ordered merge and (page_weights set) the accumulated page weights.
-cudaError_t launch_kv8_decode(bool global, const void* q, const int32_t* seq_len, const int32_t* pos, int B, int window,
-                              float scale_log2, const PagedCache8& cache, const NormArgs& nm, float* page_weights,
-                              void* out, void* ws, const DeviceState& st, cudaStream_t s);
-cudaError_t launch_evict_pages(const int32_t* seq_len, const int32_t* table, const float* weights, int B, int max_pages,
-                               int keep, int first, int last, int32_t* out_len, int32_t* out_table, float* out_weights,
-                               int32_t* freed, int32_t* n_freed, const DeviceState& st, cudaStream_t s);
 
 }  // namespace g4

@@ -1,8 +1,62 @@
 // The 8-bit paged cache's append and read-back, and the page eviction (see g4_kv8.cuh for the layout
 // and the cast).
+#include <math.h>
+
+#include <vector>
+
 #include "g4_kv8.cuh"
 
 namespace g4 {
+
+static __device__ float4 g_kv8_coarse_sliding[kRopeCoarse * kSlidingR];
+static __device__ float4 g_kv8_fine_sliding[256 * kSlidingR];
+static __device__ float4 g_kv8_coarse_global[kRopeCoarse * kGlobalR];
+static __device__ float4 g_kv8_fine_global[256 * kGlobalR];
+static Kv8Angles g_angles[64][2];   // per device and layer kind; written once, by the device's first call
+
+// Fills the tables of the current device (computed in fp64 on the host; no exception leaves).
+cudaError_t upload_kv8_angles() {
+  auto fill = [](const void* symbol, int entries, double step, int D, int R, double theta) {
+    std::vector<float4> h((size_t)entries * R);
+    for (int t = 0; t < R; ++t) {
+      const double f = pow(theta, -2.0 * t / (double)D);
+      for (int i = 0; i < entries; ++i) {
+        const double c = cos((step * i) * f), s = sin((step * i) * f);
+        const float ch = (float)c, sh = (float)s;
+        h[(size_t)i * R + t] = make_float4(ch, sh, (float)(c - ch), (float)(s - sh));
+      }
+    }
+    return cudaMemcpyToSymbol(symbol, h.data(), h.size() * sizeof(float4));
+  };
+  try {
+    cudaError_t e;
+    int dev = 0;
+    void* at[4];
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if ((e = fill(g_kv8_coarse_sliding, kRopeCoarse, 256.0, kSlidingD, kSlidingR, 1.0e4)) != cudaSuccess) return e;
+    if ((e = fill(g_kv8_fine_sliding, 256, 1.0, kSlidingD, kSlidingR, 1.0e4)) != cudaSuccess) return e;
+    if ((e = fill(g_kv8_coarse_global, kRopeCoarse, 256.0, kGlobalD, kGlobalR, 1.0e6)) != cudaSuccess) return e;
+    if ((e = fill(g_kv8_fine_global, 256, 1.0, kGlobalD, kGlobalR, 1.0e6)) != cudaSuccess) return e;
+    if ((e = cudaGetSymbolAddress(&at[0], g_kv8_coarse_sliding)) != cudaSuccess) return e;
+    if ((e = cudaGetSymbolAddress(&at[1], g_kv8_fine_sliding)) != cudaSuccess) return e;
+    if ((e = cudaGetSymbolAddress(&at[2], g_kv8_coarse_global)) != cudaSuccess) return e;
+    if ((e = cudaGetSymbolAddress(&at[3], g_kv8_fine_global)) != cudaSuccess) return e;
+    for (int k = 0; k < 2; ++k) g_angles[dev][k] = Kv8Angles{(const float4*)at[2 * k], (const float4*)at[2 * k + 1]};
+    return cudaSuccess;
+  } catch (...) {
+    return cudaErrorMemoryAllocation;
+  }
+}
+
+cudaError_t kv8_angles(bool global, Kv8Angles* out) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !g_angles[dev][global].coarse) return cudaErrorInvalidDevice;
+  *out = g_angles[dev][global];
+  return cudaSuccess;
+}
 
 namespace {
 
@@ -107,7 +161,7 @@ struct AppendArgs {
   const int32_t* seq_len;
   const int32_t* pos;   // MODE 1: RoPE position of the new token; NULL: its held index
   PagedCache8 cache;
-  RopeTables tb;
+  Kv8Angles angles;
   uint32_t* err;
   NormArgs nm;
   int parts;   // warps per row
@@ -196,8 +250,8 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const AppendArgs p) 
   // them through shared memory, two pairs to 16 bytes, [i / 2][lane] so that the reads conflict on no bank.
   float2 cs[8];
   {
-    const float4* cx = p.tb.coarse_x + (size_t)(pos >> 8) * R;
-    const float4* fx = p.tb.fine_x + (size_t)(pos & 255) * R;
+    const float4* cx = p.angles.coarse + (size_t)(pos >> 8) * R;
+    const float4* fx = p.angles.fine + (size_t)(pos & 255) * R;
     float4 c4[R / 32], f4[R / 32];
 #pragma unroll
     for (int k = 0; k < R / 32; ++k) {
@@ -574,8 +628,9 @@ cudaError_t append(AppendArgs& a, int n_rows, cudaStream_t s) {
 cudaError_t launch_kv8_append(bool global, const void* k, const void* v, const SeqRows& rows, const PagedCache8& cache,
                               const NormArgs& nm, const DeviceState& st, cudaStream_t s) {
   if (rows.T <= 0 || rows.B <= 0) return cudaSuccess;
-  AppendArgs a{(const __nv_bfloat16*)k, (const __nv_bfloat16*)v, rows, nullptr, nullptr, cache,
-               global ? st.global : st.sliding, st.err, nm, 1};
+  AppendArgs a{(const __nv_bfloat16*)k, (const __nv_bfloat16*)v, rows, nullptr, nullptr, cache, {}, st.err, nm, 1};
+  const cudaError_t e = kv8_angles(global, &a.angles);
+  if (e != cudaSuccess) return e;
   return global ? append<true, 0>(a, rows.T, s) : append<false, 0>(a, rows.T, s);
 }
 
@@ -584,8 +639,9 @@ cudaError_t launch_kv8_append_decode(bool global, const void* k_new, const void*
                                      const DeviceState& st, cudaStream_t s) {
   if (B <= 0) return cudaSuccess;
   SeqRows rows{nullptr, nullptr, nullptr, B, B};
-  AppendArgs a{(const __nv_bfloat16*)k_new, (const __nv_bfloat16*)v_new, rows, seq_len, pos, cache,
-               global ? st.global : st.sliding, st.err, nm, 1};
+  AppendArgs a{(const __nv_bfloat16*)k_new, (const __nv_bfloat16*)v_new, rows, seq_len, pos, cache, {}, st.err, nm, 1};
+  const cudaError_t e = kv8_angles(global, &a.angles);
+  if (e != cudaSuccess) return e;
   return global ? append<true, 1>(a, B, s) : append<false, 1>(a, B, s);
 }
 

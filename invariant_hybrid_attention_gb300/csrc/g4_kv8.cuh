@@ -77,6 +77,47 @@ G4_DEV uint2 kv8_codes(const float (&x)[8], uint32_t biased) {
   return make_uint2(w[0], w[1]);
 }
 
+// ---- angles ------------------------------------------------------------------------------------------
+// rope_cs from the entry-major tables (R pairs per entry; the same bits): for lanes that hold
+// consecutive pairs.
+G4_DEV float2 rope_cs_t(const RopeTables& tb, int R, int t, int pos) {
+  const float2 c = __ldg(tb.coarse_t + (size_t)(pos >> 8) * R + t);
+  const float2 m = __ldg(tb.mid_t + ((pos >> 4) & 15) * R + t);
+  const float2 f = __ldg(tb.fine_t + (pos & 15) * R + t);
+  return cmul(cmul(c, m), f);
+}
+
+// Tables of (cos, sin) in two fp32 parts (cos, sin, and what their rounding left), entry-major: coarse[c][t]
+// of 256 c f_t, fine[a][t] of a f_t, 0 <= a < 256, for the append's angles. Static, filled with the other
+// tables by the first call on a device.
+struct Kv8Angles {
+  const float4* coarse;   // [kRopeCoarse][R]
+  const float4* fine;     // [256][R]
+};
+cudaError_t upload_kv8_angles();                       // for the current device
+cudaError_t kv8_angles(bool global, Kv8Angles* out);   // after the upload
+
+// a b - c d and its kind in two fp32 parts: products exact through fma, the sum's error kept, one rounding
+// at the end.
+G4_DEV float dot2_exact(float ah, float al, float bh, float bl, float ch, float cl, float dh, float dl) {
+  const float p = ah * bh, pe = fmaf(ah, bh, -p);
+  const float q = ch * dh, qe = fmaf(ch, dh, -q);
+  const float s = p + q, z = s - p;
+  const float se = (p - (s - z)) + (q - z);
+  float low = fmaf(ah, bl, fmaf(al, bh, fmaf(ch, dl, fmaf(cl, dh, pe + qe))));
+  return s + (se + low);
+}
+
+// (cos, sin)(pos * f_t) rounded once to fp32 (nearly always to the nearest): the angle-addition formula
+// on the two-part tables. Where rope_cs carries the rounding of three table entries and two products
+// (a few 2^-24), this leaves 2^-25, so that a value next to a border between two codes falls on the
+// border's right side as often as with exactly rounded angles.
+G4_DEV float2 rope_cs_exact(float4 a, float4 b) {
+  return make_float2(dot2_exact(a.x, a.z, b.x, b.z, -a.y, -a.w, b.y, b.w),
+                     dot2_exact(a.y, a.w, b.x, b.z, a.x, a.z, b.y, b.w));
+}
+
+// ---- launches ----------------------------------------------------------------------------------------
 // Programmatic dependent launch. Every kernel of the 8-bit cache waits for the grid before it at its
 // first instruction (its end and its writes), and then lets the next grid of the stream start: back to
 // back, the launch of one hides behind the other, and nothing is read early.
@@ -127,5 +168,30 @@ struct Kv8Range {
   SeqRows rows;   // B; the rest when key_begin is NULL
   int window;     // with key_begin NULL: keys before ctx_start - window + 1 are not read (0: none)
 };
+
+// The rows' queries alone, staged into q_out as launch_append_prefill does (normed, turned, bf16); of the
+// cache only hq, hkv and max_pages are read.
+cudaError_t launch_stage_queries(bool global, const void* q, void* q_out, const SeqRows& rows, const PagedCache& cache,
+                                 const DeviceState& st, cudaStream_t s, const NormArgs& nm);
+
+
+// Writes the rows of a prefill batch into 8-bit pages.
+cudaError_t launch_kv8_append(bool global, const void* k, const void* v, const SeqRows& rows, const PagedCache8& cache,
+                              const NormArgs& nm, const DeviceState& st, cudaStream_t s);
+// Writes one new token per request at held index seq_len - 1, turned by pos (NULL: the held index).
+cudaError_t launch_kv8_append_decode(bool global, const void* k_new, const void* v_new, const int32_t* seq_len,
+                                     const int32_t* pos, int B, const PagedCache8& cache, const NormArgs& nm,
+                                     const DeviceState& st, cudaStream_t s);
+// Reads keys of 8-bit pages back into bf16 pages (dst.page_table: the destination's page table).
+cudaError_t launch_kv8_unpack(bool global, const Kv8Range& range, const PagedCache8& src, const PagedCache& dst,
+                              const DeviceState& st, cudaStream_t s);
+size_t kv8_decode_workspace_bytes(bool global, int B, int max_pages, int window, int hq, int hkv, bool pages);
+// Decode partials, ordered merge and (page_weights set) the accumulated page weights.
+cudaError_t launch_kv8_decode(bool global, const void* q, const int32_t* seq_len, const int32_t* pos, int B, int window,
+                              float scale_log2, const PagedCache8& cache, const NormArgs& nm, float* page_weights,
+                              void* out, void* ws, const DeviceState& st, cudaStream_t s);
+cudaError_t launch_evict_pages(const int32_t* seq_len, const int32_t* table, const float* weights, int B, int max_pages,
+                               int keep, int first, int last, int32_t* out_len, int32_t* out_table, float* out_weights,
+                               int32_t* freed, int32_t* n_freed, const DeviceState& st, cudaStream_t s);
 
 }  // namespace g4

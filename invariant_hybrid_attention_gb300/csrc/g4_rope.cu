@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "g4_internal.h"
+#include "g4_kv8.cuh"
 
 namespace g4 {
 
@@ -35,10 +36,6 @@ static __device__ float2 g_rope_sliding_fine_t[kRopeFine * kSlidingR];
 static __device__ float2 g_rope_global_coarse_t[kRopeCoarse * kGlobalR];
 static __device__ float2 g_rope_global_mid_t[kRopeMid * kGlobalR];
 static __device__ float2 g_rope_global_fine_t[kRopeFine * kGlobalR];
-static __device__ float4 g_rope_sliding_coarse_x[kRopeCoarse * kSlidingR];
-static __device__ float4 g_rope_sliding_fine_x[256 * kSlidingR];
-static __device__ float4 g_rope_global_coarse_x[kRopeCoarse * kGlobalR];
-static __device__ float4 g_rope_global_fine_x[256 * kGlobalR];
 static __device__ uint32_t g_error_word;
 
 namespace {
@@ -46,7 +43,6 @@ namespace {
 struct HostTables {
   std::vector<float2> coarse, mid, fine;
   std::vector<float2> coarse_t, mid_t, fine_t;   // the same values, entry-major
-  std::vector<float4> coarse_x, fine_x;          // two-part values, entry-major
 };
 
 std::vector<float2> transpose(const std::vector<float2>& a, int rows, int cols) {
@@ -66,18 +62,6 @@ void build_tables(int D, int R, double theta, HostTables& h) {
     for (int c = 0; c < kRopeCoarse; ++c) h.coarse[(size_t)t * kRopeCoarse + c] = cs((256.0 * c) * f);
     for (int a = 0; a < kRopeMid; ++a) h.mid[(size_t)t * kRopeMid + a] = cs((16.0 * a) * f);
     for (int b = 0; b < kRopeFine; ++b) h.fine[(size_t)t * kRopeFine + b] = cs((double)b * f);
-  }
-  h.coarse_x.resize((size_t)R * kRopeCoarse);
-  h.fine_x.resize((size_t)R * 256);
-  auto cs2 = [](double a) {
-    const double c = cos(a), s = sin(a);
-    const float ch = (float)c, sh = (float)s;
-    return make_float4(ch, sh, (float)(c - ch), (float)(s - sh));
-  };
-  for (int t = 0; t < R; ++t) {
-    const double f = pow(theta, -2.0 * t / (double)D);
-    for (int c = 0; c < kRopeCoarse; ++c) h.coarse_x[(size_t)c * R + t] = cs2((256.0 * c) * f);
-    for (int a = 0; a < 256; ++a) h.fine_x[(size_t)a * R + t] = cs2((double)a * f);
   }
   h.coarse_t = transpose(h.coarse, R, kRopeCoarse);
   h.mid_t = transpose(h.mid, R, kRopeMid);
@@ -104,18 +88,18 @@ cudaError_t device_state(DeviceState* st) {
   if (!g_state_ready[dev]) {
     static HostTables hs, hg;
     try {   // no exception leaves a C entry point
-      if (hg.fine_x.empty()) {
+      if (hg.fine_t.empty()) {
         build_tables(kSlidingD, kSlidingR, 1.0e4, hs);
         build_tables(kGlobalD, kGlobalR, 1.0e6, hg);
       }
     } catch (...) {
-      hg.fine_x.clear();
+      hg.fine_t.clear();
       return cudaErrorMemoryAllocation;
     }
     DeviceState s{};
     void* p = nullptr;
 #define G4_UPLOAD(sym, vec)                                                                   \
-  if ((e = cudaMemcpyToSymbol(sym, (vec).data(), (vec).size() * sizeof((vec)[0]))) != cudaSuccess) return e
+  if ((e = cudaMemcpyToSymbol(sym, (vec).data(), (vec).size() * sizeof(float2))) != cudaSuccess) return e
 #define G4_ADDR(sym, dst)                                                   \
   if ((e = cudaGetSymbolAddress(&p, sym)) != cudaSuccess) return e;         \
   dst = (const float2*)p
@@ -143,20 +127,9 @@ cudaError_t device_state(DeviceState* st) {
     G4_ADDR(g_rope_global_coarse_t, s.global.coarse_t);
     G4_ADDR(g_rope_global_mid_t, s.global.mid_t);
     G4_ADDR(g_rope_global_fine_t, s.global.fine_t);
-    G4_UPLOAD(g_rope_sliding_coarse_x, hs.coarse_x);
-    G4_UPLOAD(g_rope_sliding_fine_x, hs.fine_x);
-    G4_UPLOAD(g_rope_global_coarse_x, hg.coarse_x);
-    G4_UPLOAD(g_rope_global_fine_x, hg.fine_x);
-#define G4_ADDR4(sym, dst)                                                  \
-  if ((e = cudaGetSymbolAddress(&p, sym)) != cudaSuccess) return e;         \
-  dst = (const float4*)p
-    G4_ADDR4(g_rope_sliding_coarse_x, s.sliding.coarse_x);
-    G4_ADDR4(g_rope_sliding_fine_x, s.sliding.fine_x);
-    G4_ADDR4(g_rope_global_coarse_x, s.global.coarse_x);
-    G4_ADDR4(g_rope_global_fine_x, s.global.fine_x);
-#undef G4_ADDR4
 #undef G4_UPLOAD
 #undef G4_ADDR
+    if ((e = upload_kv8_angles()) != cudaSuccess) return e;
     const uint32_t zero = 0;
     if ((e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero))) != cudaSuccess) return e;
     if ((e = cudaGetSymbolAddress(&p, g_error_word)) != cudaSuccess) return e;
