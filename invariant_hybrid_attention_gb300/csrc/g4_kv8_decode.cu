@@ -21,16 +21,17 @@
 // Declared roundings: roped q to bf16, w to fp16 (2^-11 relative, each weight by itself), the output
 // to bf16; all sums are fp32.
 //
-// What bounds it. With many requests the page stream: 64 requests of 1k to 32k keys take 385 us in the
-// chunk kernel on a global layer (2.3 GB, 6.0 TB/s, 89% of the measured copy rate) and 86 us on a
-// sliding one (0.54 GB, 6.3 TB/s). A block's start (its queries turned and laid out, 17 us of the 385)
-// and end (the merge of its warps, 23 us) are covered only in part by the SM's other block. With few
-// requests a warp's chain through a page, about 0.8 us (scores 470 cycles, values 500, the rest between
-// them), bounds it: a lone request takes 21 us from 1024 keys up to 16384. Chunks of 2048 keys
-// would take 5% off the large batch and put 60% on the lone request; chunks of 512 the reverse (18% on,
-// 30% off). A quarter of the output per warp with the weights exchanged through shared memory (four
-// blocks an SM, no merge) and runs of two chunks per block with the pages streaming across were built
-// and measured slower (405 and 408 against 399 us).
+// What bounds it. With many requests the page stream: 64 requests of 1k to 32k keys take 396 us on a
+// global layer (2.3 GB, 5.9 TB/s, 86% of the measured copy rate; its chunks' states, 71 MB written and
+// read again, are 5% of that traffic) and 89 us on a sliding one (0.54 GB, 6.1 TB/s). A block's start
+// (its queries turned and laid out, 12 us of the 396) and end (the merge of its warps, 8 us besides the
+// states' own bytes) are covered only in part by the SM's other block. With few requests a warp's
+// chain through a page, about 0.8 us (scores 470 cycles, values 500, weights 440, the refill 150),
+// bounds it: a lone request takes 21 us from 1024 keys up to 16384. Chunks of 2048 keys would take 5%
+// off the large batch and put 60% on the lone request; chunks of 512 the reverse (15% on, 30% off). A
+// quarter of the output per warp with the weights exchanged through shared memory (four blocks an SM,
+// no merge), runs of two chunks per block with the pages streaming across, and clusters that merge
+// 2 x 1024 keys were built and measured slower (405, 408 and 419 against 399 us).
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -84,6 +85,20 @@ constexpr float kUp = 16777216.0f;   // 2^24: undoes the bytes' reading as fp16 
 
 // Two bytes of `w` as a pair of fp16 subnormals: the bytes at selector digits 0 and 2 (digit 4: zero).
 G4_DEV uint32_t codes2(uint32_t w, uint32_t selector) { return __byte_perm(w, 0u, selector); }
+// bulk_g2s whose lines are the first to leave L2: the pages stream through once, and the chunks' states,
+// written meanwhile, stay there for the merge.
+G4_DEV uint64_t evict_first_policy() {
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+G4_DEV void bulk_g2s_first(void* smem, const void* gmem, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(smem)),
+      "l"(gmem), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
 G4_DEV uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -222,11 +237,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   const size_t slot = ((size_t)b * p.cache.hq + (size_t)G * g) * p.NC + cr;   // head G g + h adds h NC
 
   uint8_t* ring = smem + warp * kStages * S::kStage;
+  const uint64_t policy = evict_first_policy();
   auto issue = [&](int n, int page) {   // lane 0: copy this warp's n-th page
     const int st = n % kStages;
     mbar_arrive_expect_tx(&full[warp][st], Blk::kBytes);
-    bulk_g2s(ring + st * S::kStage, p.cache.pages + ((size_t)page * HKV + g) * Blk::kBytes, Blk::kBytes,
-             &full[warp][st]);
+    bulk_g2s_first(ring + st * S::kStage, p.cache.pages + ((size_t)page * HKV + g) * Blk::kBytes, Blk::kBytes,
+                   &full[warp][st], policy);
   };
 #pragma unroll
   for (int n = 0; n < kStages; ++n) {
