@@ -744,6 +744,141 @@ def test_evict_passes_a_bad_sequence_on():
         assert got[1][0] == [5, 6, -1, -1] and got[3][0] == [3, 4, -1, -1]
 
 
+# ---- larger sizes and other schedules --------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_seventy_sequences(kind):
+    """More sequences than a warp looks at at once: append, read-back, prefill and decode."""
+    rng = np.random.default_rng(7)
+    rows = [int(x) for x in rng.integers(0, 5, 70)]
+    rows[3], rows[69] = 40, 33
+    ctx = [int(x) for x in rng.integers(0, 40, 70)]
+    ctx = [max(c, 1 - n) for c, n in zip(ctx, rows)]
+    r = Rows(kind, rows, ctx, seed=71, gap=1)
+    q, out, scratch = prefill(r)
+    for b in (0, 3, 33, 64, 69):
+        n = rows[b] + ctx[b]
+        for i, (got, want) in enumerate(zip(r.values(b), r.exact_parts(b))):
+            raw = i == 1 if kind == "sliding" else i == 0
+            assert_stored(got[:n], want, rounded=not raw)
+    k, two = bf16_pages(r.layer, r.cache.pages)
+    other = PagedKV(r.plan.num_pages, r.layer.n_kv_heads, r.layer.head_dim, kind == "global")
+    other.k.copy_(k.reshape(other.k.shape))
+    (other.k_rot if kind == "global" else other.v).copy_(two.reshape((other.k_rot if kind == "global" else other.v).shape))
+    ref = torch.full_like(q, 5.0)
+    g4.g4attn_prefill_attend(r.layer, q, *r.row_args(), other.desc, r.table, ref)
+    status_ok()
+    assert torch.equal(out, ref)
+    s = Step(r, weights=kind == "global")
+    s.run()
+    s.check()
+
+
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_decode_row_does_not_depend_on_the_table_width(kind):
+    """Wide page tables take the split merge: the same bits."""
+    r = Rows(kind, [3000, 70], seed=72, gap=0, window=30000)
+    r.fill()
+    s = Step(r, weights=kind == "global")
+    s.run()
+    s.check()
+    wide = torch.full((2, r.table.shape[1] + 5000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :r.table.shape[1]] = r.table
+    w = torch.zeros(wide.shape, device="cuda") if kind == "global" else None
+    ws = torch.empty(g4.g4attn_kv8_decode_workspace_bytes(r.layer, 2, wide.shape[1], kind == "global"), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.empty_like(s.out)
+    g4.g4attn_kv8_decode(r.layer, None, s.q, None, None, i32(s.lens), r.cache.desc, wide, out, ws, page_weights=w)
+    status_ok()
+    assert torch.equal(out, s.out)
+    if w is not None:
+        assert torch.equal(w[:, :r.table.shape[1]], s.weights) and (w[:, r.table.shape[1]:] == 0).all()
+
+
+@pytest.mark.parametrize("kind,window", [("global", 0), ("sliding", 262144)])
+def test_decode_longest_context(kind, window):
+    """262144 keys, the last usable position, against fp64 on the device. Beyond the tolerance above: the
+    sums run over 2^18 keys, in runs of 16 pages per warp and 256 or 512 chunks, each addition off by at
+    most 2^-24 of a partial sum that is at most sum p |v|: under 2^-15 of it in all."""
+    layer = g4.global_layer() if kind == "global" else g4.sliding_layer(window)
+    hkv, d, hq = layer.n_kv_heads, layer.head_dim, 32
+    n = 262144
+    cache = PagedKV8(layer, n // 16, fill=None)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cache.pages.random_(28, 229, generator=g)                       # codes -100 .. 100
+    cache.pages[..., -32:].random_(126, 129, generator=g)           # steps 2^-7 .. 2^-5
+    table = torch.randperm(n // 16, generator=g, device="cuda").int()[None].contiguous()
+    q = gi.bf16_normal((1, hq, d), 9).cuda()
+    out = torch.empty_like(q)
+    w = torch.zeros(table.shape, device="cuda") if kind == "global" else None
+    ws = torch.empty(g4.g4attn_kv8_decode_workspace_bytes(layer, 1, n // 16, kind == "global"), dtype=torch.uint8,
+                     device="cuda")
+    g4.g4attn_kv8_decode(layer, None, q, None, None, i32([n]), cache.desc, table, out, ws, page_weights=w)
+    status_ok()
+    roped = g4.g4attn_rope_apply(layer, q.clone(), i32([n - 1]))[0].double()
+    one, two = (x[table[0].long()].transpose(1, 2).flatten(0, 1).double() for x in untile8(cache.pages, d))
+    cols = torch.tensor(kv8.turned_columns(oracle.GLOBAL if kind == "global" else oracle.SLIDING), device="cuda")
+    pages = torch.zeros(n // 16, dtype=torch.float64, device="cuda")
+    for h in range(hkv):
+        k, v = one[:, h], (one if kind == "global" else two)[:, h]
+        if kind == "global":
+            k = k.clone()
+            k[:, cols] = two[:, h]
+        group = hq // hkv
+        p = torch.softmax(roped[group * h:group * (h + 1)] @ k.T * layer.softmax_scale, -1)
+        want, mag = p @ v, p @ v.abs()
+        peak = n * (p * v.abs().amax(-1)).amax(-1, keepdim=True)
+        got = out[0, group * h:group * (h + 1)].double()
+        over = (got - want).abs() - (2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -14) * mag + 2.0 ** -31 * peak)
+        assert (over <= 0).all(), float(over.max())
+        pages += p.sum(0).unflatten(0, (-1, 16)).sum(-1)
+    if w is not None:
+        assert torch.allclose(w[0].double(), pages, rtol=2e-5, atol=1e-9)
+
+
+def test_two_calls_at_once():
+    """Steps of two layers on two streams, each with its own workspace, over one cache."""
+    r = Rows("global", [700, 1500, 40], seed=73, gap=0)
+    r.fill()
+    want = []
+    for seed in (1, 2):
+        s = Step(r, seed=seed, weights=True)
+        for _ in range(20):
+            s.run()
+        status_ok()
+        want.append((s.out.clone(), s.weights.clone()))
+    steps = [Step(r, seed=seed, weights=True) for seed in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    lens = i32(steps[0].lens)
+    for _ in range(20):
+        for s, st in zip(steps, streams):
+            g4.g4attn_kv8_decode(r.layer, None, s.q, None, None, lens, r.cache.desc, r.table, s.out, s.ws,
+                                 page_weights=s.weights, stream=st)
+    status_ok()
+    for st in streams:
+        assert g4.g4attn_status_sync(st) == g4.G4_OK
+    for s, (out, w) in zip(steps, want):
+        assert torch.equal(s.out, out) and torch.equal(s.weights, w)
+
+
+def test_wrong_device_and_strides_are_refused():
+    r = Rows("global", [40], seed=74, gap=0)
+    r.fill()
+    s = Step(r)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        g4.g4attn_kv8_decode(r.layer, None, s.q.cpu(), None, None, i32([40]), r.cache.desc, r.table, s.out, s.ws)
+    # one row of two is dense whatever its stride says; every other column is not
+    g4.g4attn_kv8_decode(r.layer, None, torch.cat([s.q, s.q])[::2], None, None, i32([40]), r.cache.desc, r.table, s.out,
+                         s.ws)
+    status_ok()
+    with pytest.raises(ValueError, match="strided"):
+        g4.g4attn_kv8_decode(r.layer, None, torch.cat([s.q, s.q], -1)[..., ::2], None, None, i32([40]), r.cache.desc,
+                             r.table, s.out, s.ws)
+    with pytest.raises(g4.G4Error):
+        g4.g4attn_kv8_decode(r.layer, None, s.q, None, None, i32([40]), r.cache.desc, r.table, s.out, s.ws[:64])
+
+
 # ---- together -------------------------------------------------------------------------------------------
 
 def test_a_conversation_prefill_decode_evict_decode():
