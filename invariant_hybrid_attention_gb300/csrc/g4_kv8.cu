@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const AppendArgs p) 
         if (p.nm.wk) weight<D>(k, p.nm.wk, tr);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) rope_pair(k.a[e], k.b[e], cs[e]);
+      for (int e = 0; e < 8; ++e) rope_pair_apart(k.a[e], k.b[e], cs[e]);
       uint8_t* blk = page + (size_t)(g_lo + i) * Blk::kBytes;
       store_vec<D>(blk + Blk::kTile1, kv8_offset(j, tr), kv8_offset(j, R + tr), blk + Blk::kExp1 + j, k, tr == 0,
                    0xffu << (lane & 24));
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const AppendArgs p) 
         weight<D>(k, p.nm.wk, t0);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) rope_pair(k.a[i], k.b[i], cs[i]);
+      for (int i = 0; i < 8; ++i) rope_pair_apart(k.a[i], k.b[i], cs[i]);
       store_vec<D>(blk, off_a, off_b, blk + Blk::kExp0 + j, k, t0 == 0, mask);
       if (NORM && p.nm.v_norm) unit_norm<D>(v, p.nm.eps);
       store_vec<D>(blk + Blk::kTile1, off_a, off_b, blk + Blk::kExp1 + j, v, t0 == 0, mask);

@@ -78,18 +78,9 @@ G4_DEV uint2 kv8_codes(const float (&x)[8], uint32_t biased) {
 }
 
 // ---- angles ------------------------------------------------------------------------------------------
-// rope_cs from the entry-major tables (R pairs per entry; the same bits): for lanes that hold
-// consecutive pairs.
-G4_DEV float2 rope_cs_t(const RopeTables& tb, int R, int t, int pos) {
-  const float2 c = __ldg(tb.coarse_t + (size_t)(pos >> 8) * R + t);
-  const float2 m = __ldg(tb.mid_t + ((pos >> 4) & 15) * R + t);
-  const float2 f = __ldg(tb.fine_t + (pos & 15) * R + t);
-  return cmul(cmul(c, m), f);
-}
-
 // Tables of (cos, sin) in two fp32 parts (cos, sin, and what their rounding left), entry-major: coarse[c][t]
-// of 256 c f_t, fine[a][t] of a f_t, 0 <= a < 256, for the append's angles. Static, filled with the other
-// tables by the first call on a device.
+// of 256 c f_t, fine[a][t] of a f_t, 0 <= a < 256. Static, filled with the other tables by the first call
+// on a device.
 struct Kv8Angles {
   const float4* coarse;   // [kRopeCoarse][R]
   const float4* fine;     // [256][R]
@@ -115,6 +106,15 @@ G4_DEV float dot2_exact(float ah, float al, float bh, float bl, float ch, float 
 G4_DEV float2 rope_cs_exact(float4 a, float4 b) {
   return make_float2(dot2_exact(a.x, a.z, b.x, b.z, -a.y, -a.w, b.y, b.w),
                      dot2_exact(a.y, a.w, b.x, b.z, a.x, a.z, b.y, b.w));
+}
+
+// The rotation of one half-split pair with every product and sum rounded by itself. What is rounded again
+// next (to bf16, to a code) then agrees with the elementary operations on fp32 angles, border values
+// included, so that two programs that follow the definition store and compare the same numbers.
+G4_DEV void rope_pair_apart(float& lo, float& hi, float2 cs) {
+  const float a = lo, b = hi;
+  lo = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+  hi = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
 }
 
 // ---- launches ----------------------------------------------------------------------------------------

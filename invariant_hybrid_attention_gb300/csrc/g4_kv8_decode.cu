@@ -59,7 +59,8 @@ struct Shape {
   static constexpr int kStage = (Blk::kBytes + 127) / 128 * 128;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kQ = kHalves * 1024;              // q fragments: [half][2][32 lanes][16 bytes]
-  static constexpr int kSmem = kRing + kQ;
+  static constexpr int kPages = (kChunk / kPage) * 8 * 8;   // per page and head: max and sum of the page's weights
+  static constexpr int smem(bool pages) { return kRing + kQ + (pages ? kPages : 0); }
   static_assert(kRing >= kWarps * kHeads * D * 4, "the warp merge reuses the ring");
 };
 
@@ -74,9 +75,9 @@ struct Decode8Params {
   NormArgs nm;          // query norm, and the key norm's weight on a global layer's plain columns
   float* ws_ml;         // [B][hq][NC][2]: running max (log2 units) and sum
   float* ws_o;          // [B][hq][NC][D]: un-normalised output, relative to that max
-  float* ws_page;       // [B][hkv][max_pages][8]: log2 of each page's weight, or NULL
+  float* ws_page;       // [B][hkv][max_pages][8]: each page's weight relative to its chunk's max, or NULL
   int NC;
-  RopeTables tb;
+  Kv8Angles angles;
   uint32_t* err;
   unsigned long long wait_ns;
 };
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   constexpr int D = S::D;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* q_s = smem + S::kRing;
+  float2* page_s = reinterpret_cast<float2*>(q_s + S::kQ);   // [page of the chunk][8 heads]
   __shared__ uint64_t full[kWarps][kStages];
   __shared__ int abort_flag;
   __shared__ float q_scale[8], q_sum[2][8];   // per head: power of two, 128 x sum of q over the plain and turned columns
@@ -254,9 +256,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
   // as matrix fragments: lane (head, cc) of half i and step t holds columns 16 cc + 4t + {0, 2} and
   // {1, 3} of the half. One warp per head.
   float2 cs[P];               // (cos, sin) of this lane's pairs, the same for every head
-  if (t0 < Blk::R) {
+  {
+    // Exact to 2^-25, like the append's: a turned query falls on the far side of a border between two bf16
+    // numbers as rarely as with exactly rounded angles. Pairs R/32 to a lane; a global layer's eight lanes
+    // that turn fetch theirs from four lanes each.
+    constexpr int kOwn = Blk::R / 32;
+    const float4* cx = p.angles.coarse + (size_t)(rope_pos >> 8) * Blk::R + kOwn * lane;
+    const float4* fx = p.angles.fine + (size_t)(rope_pos & 255) * Blk::R + kOwn * lane;
+    float2 own[kOwn];
 #pragma unroll
-    for (int i = 0; i < P; ++i) cs[i] = rope_cs_t(p.tb, Blk::R, t0 + i, rope_pos);
+    for (int i = 0; i < kOwn; ++i) own[i] = rope_cs_exact(__ldg(cx + i), __ldg(fx + i));
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (GLOBAL) {
+        const int src = 4 * (lane & 7) + (i >> 1);
+        cs[i].x = __shfl_sync(0xffffffffu, own[i & 1].x, src);
+        cs[i].y = __shfl_sync(0xffffffffu, own[i & 1].y, src);
+      } else {
+        cs[i] = own[i % kOwn];
+      }
+    }
   }
   // Columns of the product beyond the group carry q = 0.
   for (int h = S::kHeads + warp; h < 8; h += kWarps) {   // (a sliding layer's six)
@@ -280,7 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
       if (p.nm.wq || (GLOBAL && p.nm.wk)) norm_query<GLOBAL>(p.nm, t0, a, bb);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        if (t0 < Blk::R) rope_pair(a[i], bb[i], cs[i]);
+        if (t0 < Blk::R) rope_pair_apart(a[i], bb[i], cs[i]);
         a[i] = round_bf16(a[i]);   // declared cast: roped q in bf16
         bb[i] = round_bf16(bb[i]);
       }
@@ -399,7 +418,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
       x[r] = see ? s * qs[r & 1] : -INFINITY;
       y[r] = see ? x[r] + (r < 2 ? ev_lo : ev_hi) : -INFINITY;
     }
-    float page_lse[2];
+    float2 page_ms[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float mn = fmaxf(m1[j], fmaxf(x[j], x[2 + j]));
@@ -408,18 +427,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
 #pragma unroll
         for (int w = 4; w <= 16; w <<= 1) mp = fmaxf(mp, __shfl_xor_sync(0xffffffffu, mp, w));
         mp = fmaxf(mp, kNone);
-        const float pa = ex2(x[j] - mp), pb = ex2(x[2 + j] - mp);
-        float ps = pa + pb;
+        float ps = ex2(x[j] - mp) + ex2(x[2 + j] - mp);
 #pragma unroll
         for (int w = 4; w <= 16; w <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, w);
-        page_lse[j] = mp + __log2f(ps);
+        page_ms[j] = make_float2(mp, ps);
       }
       l1[j] = fmaf(l1[j], ex2(m1[j] - mn), ex2(x[j] - mn) + ex2(x[2 + j] - mn));
       m1[j] = mn;
     }
     if (PAGES && gq == 0)
-      *reinterpret_cast<float2*>(p.ws_page + (((size_t)b * HKV + g) * p.cache.max_pages + (key0 >> 4)) * 8 + 2 * cq) =
-          make_float2(page_lse[0], page_lse[1]);
+      *reinterpret_cast<float4*>(page_s + (warp + kWarps * n) * 8 + 2 * cq) =
+          make_float4(page_ms[0].x, page_ms[0].y, page_ms[1].x, page_ms[1].y);
     // the weights' reference: moved (for the whole column) only when some key passes it by 2^8
     const bool grow = fmaxf(y[0], y[2]) > m2[0] + kLazy || fmaxf(y[1], y[3]) > m2[1] + kLazy;
     if (__any_sync(0xffffffffu, grow)) {
@@ -495,14 +513,23 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     }
   }
   __syncthreads();   // every stage has been read: reuse the ring for the warp merge
+  float* page_out = PAGES ? p.ws_page + (((size_t)b * HKV + g) * p.cache.max_pages + pg0) * 8 : nullptr;
   if (void_chunk) {   // a page outside the pool: nothing but a state that adds nothing
     if (threadIdx.x == 0) set_error(p.err, kErrPage);
     if ((int)threadIdx.x < G)
       *reinterpret_cast<float2*>(p.ws_ml + (slot + (size_t)threadIdx.x * p.NC) * 2) = make_float2(-INFINITY, 0.f);
     if (PAGES)
-      for (int i = threadIdx.x; i < n_pages * 8; i += kWarps * 32)
-        p.ws_page[(((size_t)b * HKV + g) * p.cache.max_pages + pg0) * 8 + i] = -INFINITY;
+      for (int i = threadIdx.x; i < n_pages * 8; i += kWarps * 32) page_out[i] = 0.f;
     return;
+  }
+  if (PAGES) {   // against the chunk's max: exact differences of maxima, where sums of logarithms would be rounded
+    for (int i = threadIdx.x; i < n_pages * 8; i += kWarps * 32) {
+      const int h = i & 7;
+      float M = red_m[0][h];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, red_m[w][h]);
+      page_out[i] = page_s[i].y * ex2(page_s[i].x - M);
+    }
   }
   // The warps' outputs in fragment order ([warp][row tile][lane][4]: 16 bytes a lane, no bank conflicts);
   // on sliding layers only lanes with heads (cq = 0) hold any.
@@ -659,16 +686,19 @@ __global__ void __launch_bounds__(kFinishThreads) kv8_finish_kernel(const Decode
     *reinterpret_cast<uint2*>(out + ((size_t)b * hq + h) * D + col) = pk;
     return;
   }
-  __shared__ float ref[kSlidingHq];   // log2 of each head's softmax sum
+  // 128 pages, of kSpan chunks: per head and chunk the factor 2^(chunk's max - M) / L
+  constexpr int kSpan = kFinishThreads * kPage / kChunkGlobal;
+  static_assert(kSpan * kChunkGlobal == kFinishThreads * kPage, "a block's pages are whole chunks");
+  __shared__ float factor[kSpan][kSlidingHq];
   const int unit = blockIdx.x - merge_blocks;
-  const int b = unit / blocks_per_row, i = (unit % blocks_per_row) * kFinishThreads + threadIdx.x;
+  const int b = unit / blocks_per_row, i0 = (unit % blocks_per_row) * kFinishThreads, i = i0 + threadIdx.x;
   int rope_pos;
   const int last = held_index(p.seq_len, p.pos, b, p.cache.max_pages, rope_pos);
   const int n_pages = (last >> 4) + 1;   // 0 when refused
-  if (i - (int)threadIdx.x >= n_pages) return;
+  if (i0 >= n_pages) return;
   const int HKV = p.cache.hkv, G = hq / HKV;
   const int n = min(p.NC, chunks_of(last, 0, chunk));
-  float4 x[2 * kGlobalHkv];   // this page's weights, in flight while the sums are formed
+  float4 x[2 * kGlobalHkv];   // this page's weights, in flight while the factors are formed
 #pragma unroll
   for (int g = 0; g < kGlobalHkv; ++g) {
     if (g >= HKV || i >= n_pages) continue;
@@ -678,16 +708,14 @@ __global__ void __launch_bounds__(kFinishThreads) kv8_finish_kernel(const Decode
   }
   {   // four threads a head, chunks q, q + 4, ... each, one pass with a running maximum
     const int h = threadIdx.x >> 2, q = threadIdx.x & 3;
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)b * hq + min(h, hq - 1)) * p.NC;
     float M = kNone, L = 0.f;
-    if (h < hq) {
-      const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)b * hq + h) * p.NC;
 #pragma unroll 8
-      for (int c = q; c < n; c += 4) {
-        const float2 v = ml[c];
-        const float mn = fmaxf(M, v.x);
-        L = fmaf(L, ex2(M - mn), v.x == -INFINITY ? 0.f : v.y * ex2(v.x - mn));
-        M = mn;
-      }
+    for (int c = q; c < n; c += 4) {
+      const float2 v = ml[c];
+      const float mn = fmaxf(M, v.x);
+      L = fmaf(L, ex2(M - mn), v.x == -INFINITY ? 0.f : v.y * ex2(v.x - mn));
+      M = mn;
     }
 #pragma unroll
     for (int w = 1; w <= 2; w <<= 1) {
@@ -696,10 +724,12 @@ __global__ void __launch_bounds__(kFinishThreads) kv8_finish_kernel(const Decode
       L = L * ex2(M - mn) + l2 * ex2(m2 - mn);
       M = mn;
     }
-    if (q == 0 && h < hq) ref[h] = L == 0.f ? INFINITY : M + log2f(L);   // no key: every share is 0
+    const int c = i0 / (kChunkGlobal / kPage) + q;
+    if (q < kSpan && h < hq) factor[q][h] = c < n && L != 0.f ? ex2(ml[c].x - M) / L : 0.f;   // (a NaN sum stays one)
   }
   __syncthreads();
   if (i >= n_pages) return;
+  const float* f = factor[threadIdx.x / (kChunkGlobal / kPage)];
   float sum = 0.f;
 #pragma unroll
   for (int g = 0; g < kGlobalHkv; ++g) {
@@ -708,7 +738,7 @@ __global__ void __launch_bounds__(kFinishThreads) kv8_finish_kernel(const Decode
                         x[2 * g + 1].w};
 #pragma unroll
     for (int h = 0; h < 8; ++h)
-      if (h < G) sum += ex2(v[h] - ref[G * g + h]);
+      if (h < G) sum = fmaf(v[h], f[G * g + h], sum);
   }
   page_weights[(size_t)b * p.cache.max_pages + i] += sum;
 }
@@ -745,13 +775,13 @@ cudaError_t launch(const Decode8Params& p, cudaStream_t s) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
     e = cudaFuncSetAttribute(kv8_decode_kernel<GLOBAL, PAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shape<GLOBAL>::kSmem);
+                             Shape<GLOBAL>::smem(PAGES));
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
   const long long blocks = (long long)p.NC * p.cache.hkv * p.B;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_early(kv8_decode_kernel<GLOBAL, PAGES>, (unsigned)blocks, kWarps * 32, Shape<GLOBAL>::kSmem, s, p);
+  return launch_early(kv8_decode_kernel<GLOBAL, PAGES>, (unsigned)blocks, kWarps * 32, Shape<GLOBAL>::smem(PAGES), s, p);
 }
 
 }  // namespace
@@ -786,10 +816,10 @@ cudaError_t launch_kv8_decode(bool global, const void* q, const int32_t* seq_len
   p.ws_o = (float*)w;
   w += align256(slots * D * sizeof(float));
   p.ws_page = page_weights ? (float*)w : nullptr;
-  p.tb = global ? st.global : st.sliding;
+  cudaError_t e = kv8_angles(global, &p.angles);
+  if (e != cudaSuccess) return e;
   p.err = st.err;
   p.wait_ns = wait_limit_ns();
-  cudaError_t e;
   if (!global)
     e = launch<false, false>(p, s);
   else
