@@ -149,11 +149,12 @@ G4_DEV void norm_query(const NormArgs& nm, int t0, float (&a)[Shape<GLOBAL>::D /
     for (int i = 0; i < P; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
 #pragma unroll
     for (int w = 16; w >= 1; w >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, w);
-    const float inv = __frsqrt_rn(fmaf(ss, 1.0f / (float)D, nm.eps));
+    // the definition's operations, each rounded by itself: the cast below meets borders too
+    const float root = __fsqrt_rn(__fadd_rn(ss * (1.0f / (float)D), nm.eps));   // ss / D is exact: D is a power of 2
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      a[i] = (a[i] * inv) * bf16_to_f(nm.wq[t0 + i]);
-      b[i] = (b[i] * inv) * bf16_to_f(nm.wq[D / 2 + t0 + i]);
+      a[i] = __fmul_rn(__fdiv_rn(a[i], root), bf16_to_f(nm.wq[t0 + i]));
+      b[i] = __fmul_rn(__fdiv_rn(b[i], root), bf16_to_f(nm.wq[D / 2 + t0 + i]));
     }
   }
 #pragma unroll
