@@ -550,12 +550,13 @@ __global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
   int below = 0;      // keys below T
   int round = 0;
   if (drop > 0) {
-    for (int bit = 31; bit >= 0; --bit, ++round) {
+    for (int bit = 31; bit >= 0; --bit) {
       const uint32_t c = T | (1u << bit);
       int x = 0;
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) x += key[i] < c ? 1 : 0;
-      x = block_sum(__reduce_add_sync(0xffffffffu, x), round);
+      // counted before a break: the slower warps may still read this round's array when the next is written
+      x = block_sum(__reduce_add_sync(0xffffffffu, x), round++);
       if (x <= drop) {
         T = c;
         below = x;

@@ -751,6 +751,26 @@ def test_evict_matches_the_definition(width, keep, first, last, in_place):
         assert got[3][b] == out + [-1] * (width - len(out))
 
 
+def test_evict_many_sequences_twice():
+    """Weights without ties, so that most searches end early, at every bit: each row against the definition,
+    and the same again."""
+    rng = np.random.default_rng(91)
+    B, width, keep = 400, 2050, 700
+    lens = rng.integers(16 * keep, 16 * width + 1, B).tolist()
+    table = rng.permutation(B * width).reshape(B, width).tolist()
+    w = rng.random((B, width)).astype(np.float32)
+    w[::2] = np.exp(20 * w[::2] - 10)
+    w = w.tolist()
+    first = run_evict(lens, table, w, keep, 2, 3)
+    status_ok()
+    for b in range(B):
+        n, kept, kw, out = kv8.evict(lens[b], table[b], w[b], keep, 2, 3)
+        assert first[0][b] == n and first[4][b] == len(out)
+        assert first[1][b] == kept + [-1] * (width - len(kept)) and first[3][b] == out + [-1] * (width - len(out))
+    for in_place in (False, True):
+        assert run_evict(lens, table, w, keep, 2, 3, in_place) == first
+
+
 def test_evict_passes_a_bad_sequence_on():
     table, w = [[3, 4, 5, 6]] * 3, [[1.0, 2.0, 3.0, 4.0]] * 3
     for bad in (-1, 65, 2 ** 31 - 1):
