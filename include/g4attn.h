@@ -404,11 +404,12 @@ g4_status g4attn_kv8_unpack(const g4attn_layer* layer, const int32_t* key_begin,
 /* Prefill, or one chunk of a chunked prefill, over an 8-bit cache (no counterpart in the RFC):
  * g4attn_prefill_vision whose keys and values, the new rows' own among them, are the stored 8-bit
  * values. The new rows are appended (as g4attn_kv8_append), the keys that some row sees (from
- * ctx_start - window + 1 on sliding layers, from 0 on global ones, to ctx_start + q_len - 1) are read
- * back into `scratch` (as g4attn_kv8_unpack; a caller's bf16 cache of that many pages, which layers and
- * calls ordered on one stream can share), and the attention runs over them. On return scratch holds
- * those keys' values (and zeros before the first of them in its page). norms and span may be NULL. A row's output does not depend on the batch around it
- * or on the chunks. Other arguments and errors as g4attn_prefill_vision; scratch_table: int32
+ * ctx_start - window + 1 on sliding layers, or the start of the first row's image if that lies before it,
+ * and from 0 on global ones, to ctx_start + q_len - 1) are read back into `scratch` (as g4attn_kv8_unpack;
+ * a caller's bf16 cache of that many pages, which layers and calls ordered on one stream can share), and
+ * the attention runs over them. On return scratch holds those keys' values (and zeros before the first of
+ * them in its page). norms and span may be NULL. A row's output does not depend on the batch around it or
+ * on the chunks. Other arguments and errors as g4attn_prefill_vision; scratch_table: int32
  * [B][max_pages], the scratch page of each logical page a row of sequence b sees, distinct between
  * sequences. */
 g4_status g4attn_kv8_prefill(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k,

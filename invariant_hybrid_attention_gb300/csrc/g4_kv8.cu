@@ -173,8 +173,6 @@ G4_DEV bool rows_ok(const SeqRows& r, int qs, int L, int cs) {
   return qs >= 0 && L <= r.T - qs && cs >= 0 && L <= kMaxPos && cs <= kMaxPos - L;
 }
 
-// Bound by the latency of its loads (24 warps an SM, the ALU pipe 55% busy): the 4 x 4096 sliding rows take 79
-// us (402 MB, 5.1 TB/s), the 2 x 8192 global ones 27 us (109 MB, 4 TB/s).
 // Bound by the latency of its loads (24 warps an SM, the ALU pipe 55% busy): the 4 x 4096 sliding rows take
 // 79 us (402 MB, 5.1 TB/s), the 2 x 8192 global ones 27 us (109 MB, 4 TB/s).
 // One warp per (row, share of the KV heads). The row's angles are computed once for its heads, in two-part
@@ -360,6 +358,11 @@ G4_DEV void key_range(const UnpackArgs& p, int b, int& lo, int& hi, uint32_t* er
     }
     lo = p.range.window > 0 ? max(0, cs - p.range.window + 1) : 0;
     hi = cs + L;
+    // An image that began before this chunk holds its first row, whatever other rows it holds.
+    if (lo > 0 && p.range.rows.span) {
+      const int2 s = reinterpret_cast<const int2*>(p.range.rows.span)[p.range.rows.q_start[b]];
+      if (s.x >= 0 && s.x <= cs && cs < s.y && s.y <= hi) lo = min(lo, s.x);
+    }
   }
 }
 

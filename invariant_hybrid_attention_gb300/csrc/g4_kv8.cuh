@@ -166,7 +166,8 @@ struct Kv8Range {
   const int32_t* key_begin;
   const int32_t* key_end;
   SeqRows rows;   // B; the rest when key_begin is NULL
-  int window;     // with key_begin NULL: keys before ctx_start - window + 1 are not read (0: none)
+  int window;     // with key_begin NULL: keys before ctx_start - window + 1 (and the first row's image) are not read
+                  // (0: all are)
 };
 
 // The rows' queries alone, staged into q_out as launch_append_prefill does (normed, turned, bf16); of the

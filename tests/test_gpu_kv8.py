@@ -698,6 +698,29 @@ def test_prefill_with_image_spans(kind):
         assert err.max() <= 2e-2 and err.mean() <= 2e-3
 
 
+def test_prefill_with_an_image_that_began_before_the_chunk():
+    """The image starts before the chunk's window does: its keys are read back too."""
+    r = Rows("sliding", [150, 90], [60, 70], seed=45, gap=1, window=16)
+    span = torch.zeros(r.T, 2, dtype=torch.int32)
+    images = [(5, 140), (33, 71)]
+    for b, (s0, s1) in enumerate(images):
+        span[r.start[b]:r.start[b] + s1 - r.ctx[b]] = torch.tensor([s0, s1], dtype=torch.int32)
+    q, out, scratch = prefill(r, span=span.cuda())
+    for b, (s0, _) in enumerate(images):
+        pages = r.table[b, s0 // 16:(r.ctx[b] + r.rows[b] + 15) // 16].long()
+        held = scratch.k[pages].isfinite().flatten(1).all(1)
+        assert held[:-1].all()                                  # (the last page's tail holds no key)
+    for b in range(2):
+        n, c = r.rows[b], r.ctx[b]
+        kk, vv = kv8.keys_values(r.olayer, *r.values(b))
+        roped = f64(g4.g4attn_rope_apply(r.layer, r.q[b].cuda(), i32(list(range(c, c + n)))))
+        group = r.layer.n_q_heads // r.layer.n_kv_heads
+        want = oracle.attention(roped[:, 5], kk[:, 5 // group], vv[:, 5 // group], np.arange(c, c + n), np.arange(c + n),
+                                16, r.layer.softmax_scale, [images[b]])
+        err = np.abs(f64(out[r.start[b]:r.start[b] + n, 5]) - want)
+        assert err.max() <= 2e-2 and err.mean() <= 2e-3
+
+
 def test_prefill_refuses_a_bad_sequence_and_serves_the_others():
     r = Rows("sliding", [60, 70], seed=44)
     _, ref, _ = prefill(r)
