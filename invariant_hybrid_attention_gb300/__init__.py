@@ -430,7 +430,8 @@ def g4attn_kv8_decode(layer, norms, q, k_new, v_new, seq_len, cache: g4attn_cach
     table = (B, page_table.shape[-1])
     _tensors("g4attn_kv8_decode", ("q", q, bf, qo), ("k_new", k_new, bf, kv), ("v_new", v_new, bf, kv),
              ("out", out, bf, qo), ("seq_len", seq_len, i32, (B,)), ("pos", pos, i32, (B,)),
-             ("page_table", page_table, i32, table), ("page_weights", page_weights, torch.float32, table))
+             ("page_table", page_table, i32, table), ("page_weights", page_weights, torch.float32, table),
+             ("workspace", workspace, workspace.dtype, workspace.shape))
     _check(load().g4attn_kv8_decode(ctypes.byref(layer), _opt(norms), _ptr(q), _ptr(k_new), _ptr(v_new),
                                     _ptr(seq_len), _ptr(pos), B, ctypes.byref(cache), _ptr(page_table), table[1],
                                     _ptr(page_weights), _ptr(out), _ptr(workspace),

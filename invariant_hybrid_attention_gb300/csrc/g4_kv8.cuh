@@ -125,29 +125,19 @@ G4_DEV void wait_for_grid() { asm volatile("griddepcontrol.wait;" ::: "memory");
 G4_DEV void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <class... Params, class... Args>
-cudaError_t launch_early_clusters(void (*kernel)(Params...), unsigned blocks, unsigned threads, size_t smem,
-                                  unsigned cluster, cudaStream_t s, const Args&... args) {
-  cudaLaunchAttribute attr[2] = {};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+cudaError_t launch_early(void (*kernel)(Params...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t s,
+                         const Args&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
-}
-
-template <class... Params, class... Args>
-cudaError_t launch_early(void (*kernel)(Params...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t s,
-                         const Args&... args) {
-  return launch_early_clusters(kernel, blocks, threads, smem, 1, s, args...);
 }
 
 // Paged 8-bit cache of one layer, and the head counts of the call.
@@ -174,7 +164,6 @@ struct Kv8Range {
 // cache only hq, hkv and max_pages are read.
 cudaError_t launch_stage_queries(bool global, const void* q, void* q_out, const SeqRows& rows, const PagedCache& cache,
                                  const DeviceState& st, cudaStream_t s, const NormArgs& nm);
-
 
 // Writes the rows of a prefill batch into 8-bit pages.
 cudaError_t launch_kv8_append(bool global, const void* k, const void* v, const SeqRows& rows, const PagedCache8& cache,

@@ -759,7 +759,8 @@ cudaError_t finish(const Decode8Params& p, int chunk, void* out, float* page_wei
   const long long units = (long long)p.B * p.cache.hq * (D / 128);
   const bool split = p.NC > 32;   // one warp's sixteen loads at a time would be a long chain
   const long long merge_blocks = split ? units : (units + 3) / 4;
-  const int per_row = (p.cache.max_pages + kFinishThreads - 1) / kFinishThreads;
+  const int held = p.cache.max_pages < kMaxPos / kPage ? p.cache.max_pages : kMaxPos / kPage;   // pages at most
+  const int per_row = (held + kFinishThreads - 1) / kFinishThreads;
   const long long blocks = merge_blocks + (PAGES ? (long long)p.B * per_row : 0);
   if (blocks > 0x7fffffffLL || units > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_early(split ? kv8_finish_kernel<D, PAGES, 4> : kv8_finish_kernel<D, PAGES, 1>, (unsigned)blocks,

@@ -944,6 +944,13 @@ def test_wrong_device_and_strides_are_refused():
         g4.g4attn_kv8_decode(r.layer, None, s.q, None, None, i32([40]), r.cache.desc, r.table, s.out, s.ws[:64])
 
 
+def test_a_workspace_elsewhere_is_refused():
+    r = Rows("global", [40], seed=74, gap=0)
+    s = Step(r)
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        g4.g4attn_kv8_decode(r.layer, None, s.q, None, None, i32([40]), r.cache.desc, r.table, s.out, s.ws.cpu())
+
+
 # ---- together -------------------------------------------------------------------------------------------
 
 def test_a_conversation_prefill_decode_evict_decode():

@@ -218,3 +218,6 @@ def test_binding_refuses_other_types_shapes_and_strides(lib):
         g4.g4attn_kv8_append(S, None, k.half(), k, i32, i32, i32, c8(), table)
     with pytest.raises(ValueError, match="v must"):
         g4.g4attn_kv8_append(S, None, k, k[:4], i32, i32, i32, c8(), table)
+    q, ws = torch.zeros(2, 32, 256, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace must"):      # 2^30 elements on 8 bytes
+        g4.g4attn_kv8_decode(S, None, q, None, None, i32, c8(), table, q, ws.expand(2 ** 27, 8))
