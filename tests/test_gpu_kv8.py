@@ -854,6 +854,26 @@ def test_decode_row_does_not_depend_on_the_table_width(kind):
         assert torch.equal(w[:, :r.table.shape[1]], s.weights) and (w[:, r.table.shape[1]:] == 0).all()
 
 
+def test_decode_table_wider_than_the_longest_sequence():
+    """Columns past position 262143 hold no page: they are neither read nor written."""
+    r = Rows("global", [3000, 70], seed=72, gap=0)
+    r.fill()
+    s = Step(r, weights=True)
+    s.run()
+    s.check()
+    wide = torch.full((2, 16384 + 5000), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[:, :r.table.shape[1]] = r.table
+    w = torch.full(wide.shape, 2.0, device="cuda")
+    w[:, :r.table.shape[1]] = 0.0
+    ws = torch.empty(g4.g4attn_kv8_decode_workspace_bytes(r.layer, 2, wide.shape[1], True), dtype=torch.uint8,
+                     device="cuda").fill_(255)
+    out = torch.empty_like(s.out)
+    g4.g4attn_kv8_decode(r.layer, None, s.q, None, None, i32(s.lens), r.cache.desc, wide, out, ws, page_weights=w)
+    status_ok()
+    assert torch.equal(out, s.out)
+    assert torch.equal(w[:, :r.table.shape[1]], s.weights) and (w[:, r.table.shape[1]:] == 2.0).all()
+
+
 @pytest.mark.parametrize("kind,window", [("global", 0), ("sliding", 262144)])
 def test_decode_longest_context(kind, window):
     """262144 keys, the last usable position, against fp64 on the device. Beyond the tolerance above: the
@@ -1054,3 +1074,62 @@ def test_graphs_streams_and_shared_workspace():
     g4.g4attn_kv8_decode(r.layer, None, short.q, None, None, lens, r.cache.desc, r.table, short.out, short.ws)
     status_ok()
     assert torch.equal(a.out, short.out)
+
+
+def test_captured_serving_step_between_copies_and_fills():
+    """One graph: inputs copied in, weights set to zero, decode with a new token, eviction into other buffers,
+    a copy out. Replayed over changed inputs it gives what the calls give one by one."""
+    r = Rows("global", [300, 1100, 40], seed=62, gap=0)
+    r.fill()
+    B, width = 3, r.table.shape[1] + 1
+    table = torch.full((B, width), -1, dtype=torch.int32)
+    table[:, :r.table.shape[1]] = r.table.cpu()
+    pool = PagedKV8(r.layer, r.plan.num_pages + B)
+    pool.pages[:r.plan.num_pages] = r.cache.pages
+    lens = [n + 1 for n in r.rows]
+    for b in range(B):
+        if r.rows[b] % 16 == 0:
+            table[b, r.rows[b] // 16] = r.plan.num_pages + b
+    table, lens = table.cuda(), i32(lens)
+    ws = torch.empty(g4.g4attn_kv8_decode_workspace_bytes(r.layer, B, width, True), dtype=torch.uint8, device="cuda")
+
+    def buffers():
+        z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")   # noqa: E731
+        return dict(q=torch.zeros(B, 32, 512, dtype=torch.bfloat16, device="cuda"),
+                    k=torch.zeros(B, 4, 512, dtype=torch.bfloat16, device="cuda"),
+                    out=torch.zeros(B, 32, 512, dtype=torch.bfloat16, device="cuda"),
+                    w=torch.zeros(B, width, device="cuda"), n_len=z(B), n_table=z(B, width),
+                    n_w=torch.zeros(B, width, device="cuda"), freed=z(B, width), nf=z(B), copy=z(B, width))
+
+    def step(x, q, k):
+        x["q"].copy_(q)
+        x["k"].copy_(k)
+        x["w"].zero_()
+        g4.g4attn_kv8_decode(r.layer, None, x["q"], x["k"], None, lens, pool.desc, table, x["out"], ws,
+                             page_weights=x["w"])
+        g4.g4attn_evict_pages(lens, table, x["w"], 10, 1, 2, x["n_len"], x["n_table"], x["n_w"], x["freed"], x["nf"])
+        x["copy"].copy_(x["n_table"])
+
+    q_in, k_in = torch.zeros(B, 32, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(
+        B, 4, 512, dtype=torch.bfloat16, device="cuda")
+    got, want = buffers(), buffers()
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        step(got, q_in, k_in)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step(got, q_in, k_in)
+    for seed in range(4):
+        q, k = gi.bf16_normal((B, 32, 512), 70 + seed).cuda(), gi.bf16_normal((B, 4, 512), 80 + seed).cuda()
+        step(want, q, k)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            q_in.copy_(q)
+            k_in.copy_(k)
+            graph.replay()
+            graph.replay()
+        status_ok()
+        for name in want:
+            assert torch.equal(got[name], want[name]), name
