@@ -92,9 +92,13 @@ G4_DEV Vec<D> widen(const Raw& raw) {
   return v;
 }
 
-// x / sqrt(mean(x^2) + eps), over the D/16 lanes of the vector; returns the factor.
+// sqrt(mean(x^2) + eps) over the D/16 lanes of the vector, and its reciprocal.
+struct Norm {
+  float root, inv;
+};
+
 template <int D>
-G4_DEV float unit_norm(Vec<D>& v, float eps) {
+G4_DEV Norm norm_of(const Vec<D>& v, float eps) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ss = fmaf(v.a[i], v.a[i], ss);
@@ -102,13 +106,25 @@ G4_DEV float unit_norm(Vec<D>& v, float eps) {
   for (int i = 0; i < 8; ++i) ss = fmaf(v.b[i], v.b[i], ss);
 #pragma unroll
   for (int o = 1; o < D / 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float inv = __frsqrt_rn(fmaf(ss, 1.0f / (float)D, eps));   // ss / D is exact: D is a power of 2
+  const float root = __fsqrt_rn(__fadd_rn(ss * (1.0f / (float)D), eps));   // ss / D is exact: D is a power of 2
+  // an infinite root divides every number to 0: with root 0 the quotient below is x 0
+  return Norm{root == INFINITY ? 0.f : root, __frcp_rn(root)};
+}
+
+// x / root to the nearest, by Markstein's method: the product with the rounded reciprocal, corrected by its
+// exact remainder. What is rounded to a code next then agrees with the definition's division.
+G4_DEV float over(float x, Norm n) {
+  const float q = x * n.inv;
+  return fmaf(fmaf(-q, n.root, x), n.inv, q);
+}
+
+template <int D>
+G4_DEV void divide(Vec<D>& v, Norm n) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    v.a[i] *= inv;
-    v.b[i] *= inv;
+    v.a[i] = over(v.a[i], n);
+    v.b[i] = over(v.b[i], n);
   }
-  return inv;
 }
 
 template <int D>
@@ -276,12 +292,15 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const AppendArgs p) 
   }
   const uint32_t off_a = kv8_offset(j, t0), off_b = kv8_offset(j, D / 2 + t0);
   if (GLOBAL) {
-    float inv[4] = {1.f, 1.f, 1.f, 1.f};   // 1 / norm of each head
+    Norm norm[4];   // of each head
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i >= per) break;
       Vec<D> k = widen<D>(raw[i]);
-      if (NORM && p.nm.v_norm) inv[i] = unit_norm<D>(k, p.nm.eps);
+      if (NORM && p.nm.v_norm) {
+        norm[i] = norm_of<D>(k, p.nm.eps);
+        divide<D>(k, norm[i]);
+      }
       uint8_t* blk = page + (size_t)(g_lo + i) * Blk::kBytes;
       store_vec<D>(blk, off_a, off_b, blk + Blk::kExp0 + j, k, lane == 0, 0xffffffffu);
     }
@@ -289,14 +308,7 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const AppendArgs p) 
     if (i < per) {
       Vec<D> k = widen<D>(raw_turned);
       if (NORM) {
-        if (p.nm.v_norm) {
-          const float s = i == 0 ? inv[0] : i == 1 ? inv[1] : i == 2 ? inv[2] : inv[3];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            k.a[e] *= s;
-            k.b[e] *= s;
-          }
-        }
+        if (p.nm.v_norm) divide<D>(k, i == 0 ? norm[0] : i == 1 ? norm[1] : i == 2 ? norm[2] : norm[3]);
         if (p.nm.wk) weight<D>(k, p.nm.wk, tr);
       }
 #pragma unroll
@@ -317,13 +329,13 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const AppendArgs p) 
         raw_v = load_raw<D>(v_row + (size_t)(g + 2) * D, t0);
       }
       if (NORM && p.nm.wk) {
-        unit_norm<D>(k, p.nm.eps);
+        divide<D>(k, norm_of<D>(k, p.nm.eps));
         weight<D>(k, p.nm.wk, t0);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) rope_pair_apart(k.a[i], k.b[i], cs[i]);
       store_vec<D>(blk, off_a, off_b, blk + Blk::kExp0 + j, k, t0 == 0, mask);
-      if (NORM && p.nm.v_norm) unit_norm<D>(v, p.nm.eps);
+      if (NORM && p.nm.v_norm) divide<D>(v, norm_of<D>(v, p.nm.eps));
       store_vec<D>(blk + Blk::kTile1, off_a, off_b, blk + Blk::kExp1 + j, v, t0 == 0, mask);
     }
   }

@@ -153,6 +153,30 @@ def test_append_stores_the_definition(kind, tp, normed):
             assert_stored(got[:n], want, rounded=not raw)
 
 
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_append_norms_by_a_rounded_division(kind):
+    """Small whole numbers: their squares' sum is exact in any order, so mean + eps, its root and the quotient
+    are one elementary fp32 operation each, and every code is fixed. A mean past fp32's range gives zeros,
+    an infinity a NaN vector."""
+    r = Rows(kind, [150, 33], seed=3, norms=Norms(kind, 6))
+    x = r.k if kind == "global" else r.v
+    rng = np.random.default_rng(3)
+    for t in x:
+        t.copy_(torch.from_numpy(rng.integers(-15, 16, t.shape).astype(np.float32)).bfloat16())
+    x[0][5], x[0][6] = x[0][5] * 1e30, x[0][6] * 1e-30
+    x[1][7, 0, 9] = float("inf")
+    r.fill()
+    status_ok()
+    for b in range(2):
+        a = x[b].float().numpy()
+        with np.errstate(over="ignore", invalid="ignore"):
+            mean = np.square(a).sum(-1, keepdims=True, dtype=np.float32) / np.float32(a.shape[-1])
+            quotient = a / np.sqrt(mean + np.float32(1e-6))
+        got = r.values(b)[0 if kind == "global" else 1]
+        assert np.array_equal(got, kv8.stored(quotient.astype(np.float64)), equal_nan=True)
+    assert (r.values(0)[0 if kind == "global" else 1][5] == 0).all()
+
+
 def test_append_far_positions():
     """The last usable position, where fp32 angles would be 0.02 rad off."""
     for kind in ("sliding", "global"):
