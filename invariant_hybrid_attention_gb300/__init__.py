@@ -340,27 +340,50 @@ def g4attn_merge_partials(layer, o_parts, ml_parts, q_start, q_len, out, stream=
 
 # ---- the 8-bit paged cache ----------------------------------------------------------------------------
 # The kernels take dense tensors of one type on the current device; these calls check that, since a
-# raw pointer cannot say otherwise.
+# raw pointer cannot say otherwise. A small step's kernels run for 7 us, so the checks are one pass over the
+# arguments, with torch's names looked up once.
+
+_names = None   # (bfloat16, int32, float32, the current device, a device's current raw stream)
+
+
+def _torch_names():
+    global _names
+    import torch
+    _names = (torch.bfloat16, torch.int32, torch.float32, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    return _names
+
 
 def make_cache8(pages, num_pages: int) -> g4attn_cache8:
     return g4attn_cache8(_ptr(pages), int(num_pages), PAGE_SIZE)
 
 
-def _tensors(what: str, *specs):
-    """Checks (name, tensor or None, dtype, shape) of a call; None and raw addresses pass."""
-    import torch
-    here = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
-    elsewhere = None
+def _pointers(what: str, stream, specs):
+    """The addresses of a call's tensors, given as (name, tensor, dtype, shape), and of its stream (None: the
+    current one). None and raw addresses pass unchecked; the first one is a tensor."""
+    _, _, _, device, raw_stream = _names
+    here = specs[0][1].get_device()
+    if here >= 0:
+        here = device()
+    out = []
     for name, t, dtype, shape in specs:
         if t is None or t.__class__ is int:
+            out.append(t)
             continue
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != here or here < 0 or not t.is_contiguous():
+            _refuse(what, specs, here)
+        out.append(t.data_ptr())
+    out.append(raw_stream(here) if stream is None else _stream(stream))
+    return out
+
+
+def _refuse(what: str, specs, here: int):
+    given = [x for x in specs if x[1] is not None and x[1].__class__ is not int]
+    for name, t, dtype, shape in given:
         if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{what}: {name} must be a dense {dtype} tensor of shape {tuple(shape)}, got "
                              f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (strided)'}")
-        if t.get_device() != here or here < 0:
-            elsewhere = elsewhere or (name, t.device)
-    if elsewhere:
-        raise ValueError(f"{what}: {elsewhere[0]} is on {elsewhere[1]}, not on the current CUDA device")
+    name, t = next((name, t) for name, t, _, _ in given if here < 0 or t.get_device() != here)
+    raise ValueError(f"{what}: {name} is on {t.device}, not on the current CUDA device")
 
 
 def _opt(s):
@@ -373,45 +396,45 @@ def g4attn_kv8_page_bytes(layer) -> int:
 
 def g4attn_kv8_append(layer, norms, k, v, q_start, q_len, ctx_start, cache: g4attn_cache8, page_table, stream=None):
     """g4attn_kv_append_normed into an 8-bit cache; norms may be None."""
-    import torch
-    T, B, bf, i32 = k.shape[0], q_start.shape[0], torch.bfloat16, torch.int32
-    kv = (T, layer.n_kv_heads, layer.head_dim)
-    _tensors("g4attn_kv8_append", ("k", k, bf, kv), ("v", v, bf, kv), ("q_start", q_start, i32, (B,)),
-             ("q_len", q_len, i32, (B,)), ("ctx_start", ctx_start, i32, (B,)),
-             ("page_table", page_table, i32, (B, page_table.shape[-1])))
-    _check(load().g4attn_kv8_append(ctypes.byref(layer), _opt(norms), _ptr(k), _ptr(v), T, _ptr(q_start), _ptr(q_len),
-                                    _ptr(ctx_start), B, ctypes.byref(cache), _ptr(page_table), page_table.shape[1],
-                                    _stream(stream)), "g4attn_kv8_append")
+    bf, i32, _, _, _ = _names or _torch_names()
+    T, B, width = k.shape[0], q_start.shape[0], page_table.shape[-1]
+    kv, rows = (T, layer.n_kv_heads, layer.head_dim), (B,)
+    k, v, q_start, q_len, ctx_start, page_table, stream = _pointers("g4attn_kv8_append", stream, (
+        ("k", k, bf, kv), ("v", v, bf, kv), ("q_start", q_start, i32, rows), ("q_len", q_len, i32, rows),
+        ("ctx_start", ctx_start, i32, rows), ("page_table", page_table, i32, (B, width))))
+    _check((_lib or load()).g4attn_kv8_append(ctypes.byref(layer), _opt(norms), k, v, T, q_start, q_len, ctx_start, B,
+                                              ctypes.byref(cache), page_table, width, stream), "g4attn_kv8_append")
 
 
 def g4attn_kv8_unpack(layer, key_begin, key_end, cache: g4attn_cache8, page_table, out: g4attn_cache, out_table,
                       stream=None):
     """Reads keys key_begin[b] .. key_end[b]-1 back as bf16 pages of `out` (through out_table)."""
-    import torch
-    B, i32 = key_begin.shape[0], torch.int32
-    table = (B, page_table.shape[-1])
-    _tensors("g4attn_kv8_unpack", ("key_begin", key_begin, i32, (B,)), ("key_end", key_end, i32, (B,)),
-             ("page_table", page_table, i32, table), ("out_table", out_table, i32, table))
-    _check(load().g4attn_kv8_unpack(ctypes.byref(layer), _ptr(key_begin), _ptr(key_end), B, ctypes.byref(cache),
-                                    _ptr(page_table), ctypes.byref(out), _ptr(out_table), table[1], _stream(stream)),
+    _, i32, _, _, _ = _names or _torch_names()
+    B, width = key_begin.shape[0], page_table.shape[-1]
+    rows, table = (B,), (B, width)
+    key_begin, key_end, page_table, out_table, stream = _pointers("g4attn_kv8_unpack", stream, (
+        ("key_begin", key_begin, i32, rows), ("key_end", key_end, i32, rows), ("page_table", page_table, i32, table),
+        ("out_table", out_table, i32, table)))
+    _check((_lib or load()).g4attn_kv8_unpack(ctypes.byref(layer), key_begin, key_end, B, ctypes.byref(cache),
+                                              page_table, ctypes.byref(out), out_table, width, stream),
            "g4attn_kv8_unpack")
 
 
 def g4attn_kv8_prefill(layer, norms, q, k, v, q_start, q_len, ctx_start, cache: g4attn_cache8, page_table,
                        scratch: g4attn_cache, scratch_table, out, span=None, stream=None):
     """A prefill (or chunk) over an 8-bit cache; scratch: a bf16 cache for the keys its rows see."""
-    import torch
-    T, B, bf, i32 = q.shape[0], q_start.shape[0], torch.bfloat16, torch.int32
+    bf, i32, _, _, _ = _names or _torch_names()
+    T, B, width = q.shape[0], q_start.shape[0], page_table.shape[-1]
     qo, kv = (T, layer.n_q_heads, layer.head_dim), (T, layer.n_kv_heads, layer.head_dim)
-    table = (B, page_table.shape[-1])
-    _tensors("g4attn_kv8_prefill", ("q", q, bf, qo), ("k", k, bf, kv), ("v", v, bf, kv), ("out", out, bf, qo),
-             ("q_start", q_start, i32, (B,)), ("q_len", q_len, i32, (B,)), ("ctx_start", ctx_start, i32, (B,)),
-             ("page_table", page_table, i32, table), ("scratch_table", scratch_table, i32, table),
-             ("span", span, i32, (T, 2)))
-    _check(load().g4attn_kv8_prefill(ctypes.byref(layer), _opt(norms), _ptr(q), _ptr(k), _ptr(v), T, _ptr(q_start),
-                                     _ptr(q_len), _ptr(ctx_start), B, _ptr(span), ctypes.byref(cache),
-                                     _ptr(page_table), ctypes.byref(scratch), _ptr(scratch_table), table[1], _ptr(out),
-                                     _stream(stream)), "g4attn_kv8_prefill")
+    rows, table = (B,), (B, width)
+    qp, k, v, q_start, q_len, ctx_start, span, page_table, scratch_table, op, stream = _pointers(
+        "g4attn_kv8_prefill", stream, (
+            ("q", q, bf, qo), ("k", k, bf, kv), ("v", v, bf, kv), ("q_start", q_start, i32, rows),
+            ("q_len", q_len, i32, rows), ("ctx_start", ctx_start, i32, rows), ("span", span, i32, (T, 2)),
+            ("page_table", page_table, i32, table), ("scratch_table", scratch_table, i32, table), ("out", out, bf, qo)))
+    _check((_lib or load()).g4attn_kv8_prefill(ctypes.byref(layer), _opt(norms), qp, k, v, T, q_start, q_len, ctx_start,
+                                               B, span, ctypes.byref(cache), page_table, ctypes.byref(scratch),
+                                               scratch_table, width, op, stream), "g4attn_kv8_prefill")
     return out
 
 
@@ -424,33 +447,32 @@ def g4attn_kv8_decode(layer, norms, q, k_new, v_new, seq_len, cache: g4attn_cach
                       pos=None, page_weights=None, stream=None):
     """One decode step over an 8-bit cache. k_new None: the newest token is in the cache already; pos:
     RoPE positions of sequences that lost pages; page_weights: accumulated per page (global layers)."""
-    import torch
-    B, bf, i32 = q.shape[0], torch.bfloat16, torch.int32
+    bf, i32, f32, _, _ = _names or _torch_names()
+    B, width = q.shape[0], page_table.shape[-1]
     qo, kv = (B, layer.n_q_heads, layer.head_dim), (B, layer.n_kv_heads, layer.head_dim)
-    table = (B, page_table.shape[-1])
-    _tensors("g4attn_kv8_decode", ("q", q, bf, qo), ("k_new", k_new, bf, kv), ("v_new", v_new, bf, kv),
-             ("out", out, bf, qo), ("seq_len", seq_len, i32, (B,)), ("pos", pos, i32, (B,)),
-             ("page_table", page_table, i32, table), ("page_weights", page_weights, torch.float32, table),
-             ("workspace", workspace, workspace.dtype, workspace.shape))
-    _check(load().g4attn_kv8_decode(ctypes.byref(layer), _opt(norms), _ptr(q), _ptr(k_new), _ptr(v_new),
-                                    _ptr(seq_len), _ptr(pos), B, ctypes.byref(cache), _ptr(page_table), table[1],
-                                    _ptr(page_weights), _ptr(out), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)),
-           "g4attn_kv8_decode")
+    rows, table = (B,), (B, width)
+    q, k_new, v_new, seq_len, pos, page_table, page_weights, op, work, stream = _pointers("g4attn_kv8_decode", stream, (
+        ("q", q, bf, qo), ("k_new", k_new, bf, kv), ("v_new", v_new, bf, kv), ("seq_len", seq_len, i32, rows),
+        ("pos", pos, i32, rows), ("page_table", page_table, i32, table), ("page_weights", page_weights, f32, table),
+        ("out", out, bf, qo), ("workspace", workspace, workspace.dtype, workspace.shape)))
+    _check((_lib or load()).g4attn_kv8_decode(ctypes.byref(layer), _opt(norms), q, k_new, v_new, seq_len, pos, B,
+                                              ctypes.byref(cache), page_table, width, page_weights, op, work,
+                                              workspace.nbytes, stream), "g4attn_kv8_decode")
     return out
 
 
 def g4attn_evict_pages(seq_len, page_table, page_weights, keep_pages: int, first_pages: int, last_pages: int,
                        out_seq_len, out_table, out_weights, freed, n_freed, stream=None):
     """Evicts each sequence's lightest pages down to keep_pages; the out_ tensors may be the inputs."""
-    import torch
-    B, i32, f32 = seq_len.shape[0], torch.int32, torch.float32
-    table = (B, page_table.shape[-1])
-    _tensors("g4attn_evict_pages", ("seq_len", seq_len, i32, (B,)), ("page_table", page_table, i32, table),
-             ("page_weights", page_weights, f32, table), ("out_seq_len", out_seq_len, i32, (B,)),
-             ("out_table", out_table, i32, table), ("out_weights", out_weights, f32, table),
-             ("freed", freed, i32, table), ("n_freed", n_freed, i32, (B,)))
-    _check(load().g4attn_evict_pages(_ptr(seq_len), _ptr(page_table), _ptr(page_weights), B, table[1], int(keep_pages),
-                                     int(first_pages), int(last_pages), _ptr(out_seq_len), _ptr(out_table),
-                                     _ptr(out_weights), _ptr(freed), _ptr(n_freed), _stream(stream)),
-           "g4attn_evict_pages")
+    _, i32, f32, _, _ = _names or _torch_names()
+    B, width = seq_len.shape[0], page_table.shape[-1]
+    rows, table = (B,), (B, width)
+    seq_len, page_table, page_weights, out_seq_len, out_table, out_weights, freed, n_freed, stream = _pointers(
+        "g4attn_evict_pages", stream, (
+            ("seq_len", seq_len, i32, rows), ("page_table", page_table, i32, table),
+            ("page_weights", page_weights, f32, table), ("out_seq_len", out_seq_len, i32, rows),
+            ("out_table", out_table, i32, table), ("out_weights", out_weights, f32, table),
+            ("freed", freed, i32, table), ("n_freed", n_freed, i32, rows)))
+    _check((_lib or load()).g4attn_evict_pages(seq_len, page_table, page_weights, B, width, int(keep_pages),
+                                               int(first_pages), int(last_pages), out_seq_len, out_table, out_weights,
+                                               freed, n_freed, stream), "g4attn_evict_pages")
