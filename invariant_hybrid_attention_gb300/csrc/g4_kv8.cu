@@ -498,10 +498,9 @@ __global__ void __launch_bounds__(256) kv8_unpack_kernel(const UnpackArgs p) {
 // One block per sequence, warp w and lane l hold pages (w * ITEMS + i) * 32 + l, i < ITEMS, in registers, so
 // the outputs may be the inputs. The n - keep lightest evictable pages leave. The weight T of the last
 // one to leave is found bit by bit from the top: the number of keys below a candidate is a compare per
-// key, a ballot-free warp sum and one barrier (the per-warp counts alternate between two arrays). Of
-// the pages of weight T the first in index order leave. Bound by those rounds: 64 rows of up to 16384 pages
-// take 19 us, 3 of 131 5 us. Two block-wide scans of per-warp counts then
-// give every page its place.
+// key, a warp sum and one barrier, until it is exact. Of the pages of weight T the first in index order
+// leave. Two block-wide scans of per-warp counts then give every page its place. Bound by the rounds of the
+// search: 64 rows of up to 16384 pages take 18 us (21 with the search as a loop), 3 of 131 5 us.
 G4_DEV uint32_t ordered_bits(float w) {   // unsigned order = the order of the floats; NaN above all
   const uint32_t u = __float_as_uint(w);
   if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
@@ -524,7 +523,7 @@ struct EvictArgs {
 
 template <int ITEMS>
 __global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
-  __shared__ int counts[2][32];
+  __shared__ int counts[4][32];   // by bit parity; the ties; the leaving: none is written while it may be read
   wait_for_grid();
   let_next_grid_start();
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
@@ -543,17 +542,17 @@ __global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
   const int n = bad ? p.max_pages : (len + kPage - 1) >> 4;   // a bad row is passed on as it is
   const int drop = bad ? 0 : max(0, n - p.keep);
   const int e0 = p.first, e1 = n - p.last;   // evictable pages [e0, e1): at least drop, as keep >= first + last
-  // The sum over the block of one count per warp, in every thread; `round` alternates the arrays.
-  auto block_sum = [&](int x, int round) {
-    if (lane == 0) counts[round & 1][warp] = x;
+  // The sum over the block of one count per warp, in every thread.
+  auto block_sum = [&](int x, int array) {
+    if (lane == 0) counts[array][warp] = x;
     __syncthreads();
-    return __reduce_add_sync(0xffffffffu, lane < n_warps ? counts[round & 1][lane] : 0);
+    return __reduce_add_sync(0xffffffffu, lane < n_warps ? counts[array][lane] : 0);
   };
   // Exclusive sum over the warps before this one.
-  auto before = [&](int x, int round) {
-    if (lane == 0) counts[round & 1][warp] = x;
+  auto before = [&](int x, int array) {
+    if (lane == 0) counts[array][warp] = x;
     __syncthreads();
-    return __reduce_add_sync(0xffffffffu, lane < warp ? counts[round & 1][lane] : 0);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? counts[array][lane] : 0);
   };
   uint32_t key[ITEMS];
 #pragma unroll
@@ -563,15 +562,14 @@ __global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
   }
   uint32_t T = 0;     // at last the drop-th smallest key, or any value with exactly drop keys below it
   int below = 0;      // keys below T
-  int round = 0;
   if (drop > 0) {
+#pragma unroll
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t c = T | (1u << bit);
       int x = 0;
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) x += key[i] < c ? 1 : 0;
-      // counted before a break: the slower warps may still read this round's array when the next is written
-      x = block_sum(__reduce_add_sync(0xffffffffu, x), round++);
+      x = block_sum(__reduce_add_sync(0xffffffffu, x), bit & 1);
       if (x <= drop) {
         T = c;
         below = x;
@@ -588,7 +586,7 @@ __global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
     tie_mask[i] = __ballot_sync(0xffffffffu, drop > 0 && at >= e0 && at < e1 && key[i] == T);
     x += __popc(tie_mask[i]);
   }
-  int tie = before(x, round++);
+  int tie = before(x, 2);
   const unsigned lower = (1u << lane) - 1u;
   unsigned leave[ITEMS];
   x = 0;
@@ -601,7 +599,7 @@ __global__ void __launch_bounds__(1024) evict_pages_kernel(const EvictArgs p) {
     leave[i] = __ballot_sync(0xffffffffu, out);
     x += __popc(leave[i]);
   }
-  int gone = before(x, round);
+  int gone = before(x, 3);
   const int kept = n - drop;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
