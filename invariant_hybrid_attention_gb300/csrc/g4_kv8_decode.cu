@@ -21,10 +21,10 @@
 // Declared roundings: roped q to bf16, w to fp16 (2^-11 relative, each weight by itself), the output
 // to bf16; all sums are fp32.
 //
-// What bounds it. With many requests the page stream: 64 requests of 1k to 32k keys take 396 us on a
+// What bounds it. With many requests the page stream: 64 requests of 1k to 32k keys take 393 us on a
 // global layer (2.3 GB, 5.9 TB/s, 86% of the measured copy rate; its chunks' states, 71 MB written and
-// read again, are 5% of that traffic) and 89 us on a sliding one (0.54 GB, 6.1 TB/s). A block's start
-// (its queries turned and laid out, 12 us of the 396) and end (the merge of its warps, 8 us besides the
+// read again, are 5% of that traffic) and 91 us on a sliding one (0.54 GB, 5.9 TB/s). A block's start
+// (its queries turned and laid out, 12 us of the 393) and end (the merge of its warps, 8 us besides the
 // states' own bytes) are covered only in part by the SM's other block. With few requests a warp's
 // chain through a page, about 0.8 us (scores 470 cycles, values 500, weights 440, the refill 150),
 // bounds it: a lone request takes 21 us from 1024 keys up to 16384. Chunks of 2048 keys would take 5%
