@@ -878,6 +878,31 @@ def test_decode_row_does_not_depend_on_the_table_width(kind):
         assert torch.equal(w[:, :r.table.shape[1]], s.weights) and (w[:, r.table.shape[1]:] == 0).all()
 
 
+@pytest.mark.parametrize("kind,limit", [("global", 64), ("sliding", 32)])
+def test_decode_of_one_chunk_gives_the_merged_bits(kind, limit):
+    """Tables of one chunk are served without a merge, into q itself here: the bits of a wider table's call,
+    zeros for a request that is refused or has a page outside the pool."""
+    r = Rows(kind, [16 * limit, 1, 16, 333, 40, 50], seed=77, gap=0, norms=Norms(kind, 3))
+    r.fill()
+    wide = r.table.clone()
+    wide[4, 1] = r.plan.num_pages
+    wide = torch.cat([wide, torch.full((6, limit + 1 - wide.shape[1]), -1, dtype=torch.int32, device="cuda")], 1)
+    lens = i32([16 * limit, 1, 16, 333, 40, 0])
+    q = gi.bf16_normal((6, r.layer.n_q_heads, r.layer.head_dim), 9).cuda()
+    got = []
+    for width in (limit, limit + 1):
+        table, out = wide[:, :width].contiguous(), q.clone()
+        ws = torch.empty(g4.g4attn_kv8_decode_workspace_bytes(r.layer, 6, width), dtype=torch.uint8, device="cuda")
+        g4.g4attn_kv8_decode(r.layer, r.norms.arg, out, None, None, lens, r.cache.desc, table, out, ws)
+        torch.cuda.synchronize()
+        assert g4.g4attn_status_sync() == g4.G4_ERR_DEVICE
+        got.append(out)
+    assert torch.equal(got[0], got[1])
+    group = r.layer.n_q_heads // r.layer.n_kv_heads
+    assert (got[0][5] == 0).all() and (got[0][4].unflatten(0, (-1, group)) == 0).all()
+    assert (got[0][:4] != 0).flatten(1).any(1).all()
+
+
 def test_decode_table_wider_than_the_longest_sequence():
     """Columns past position 262143 hold no page: they are neither read nor written."""
     r = Rows("global", [3000, 70], seed=72, gap=0)
