@@ -17,9 +17,9 @@
 //            fp16's smallest step is 2^-38 of that);
 //   weights  P.V needs w_j = p_j 2^ev_j c_j: the power joins the exponent of the softmax weight,
 //            w_j = 2^(x_j + ev_j - m2 + 7) in fp16, with a running maximum m2 of x_j + ev_j of its
-//            own, apart from the maximum m1 that the sum of p_j = 2^(x_j - m1) is kept with. m2 moves
-//            only when it grows by more than 2^8, so w_j <= 2^15, and a weight is lost only below
-//            2^-32 of the largest.
+//            own, apart from the maximum m1 that the sum of p_j = 2^(x_j - m1) is kept with. A head's
+//            m2 moves only when its own maximum grows by more than 2^8, so w_j <= 2^15, and a weight
+//            is lost only below 2^-32 of the largest.
 // Declared roundings: roped q to bf16, w to fp16 (2^-11 relative, each weight by itself), the output
 // to bf16; all sums are fp32.
 //
@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     if (PAGES && gq == 0)
       *reinterpret_cast<float4*>(page_s + (warp + kWarps * n) * 8 + 2 * cq) =
           make_float4(page_ms[0].x, page_ms[0].y, page_ms[1].x, page_ms[1].y);
-    // the weights' reference: moved (for the whole column) only when some key passes it by 2^8
+    // the weights' reference: a head's moves only when one of its own keys passes it by 2^8, whatever the
+    // other columns do (a head's bits are those it gets in a rank's slice); the vote only skips the block
     const bool grow = fmaxf(y[0], y[2]) > m2[0] + kLazy || fmaxf(y[1], y[3]) > m2[1] + kLazy;
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
         float mn = fmaxf(y[j], y[2 + j]);
 #pragma unroll
         for (int w = 4; w <= 16; w <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
-        mn = fmaxf(mn, m2[j]);
+        mn = mn > m2[j] + kLazy ? mn : m2[j];
         const float al = ex2(m2[j] - mn);
         m2[j] = mn;
 #pragma unroll
