@@ -44,6 +44,13 @@ struct SeqRows {
   bool by_cost = false;
 };
 
+// A sequence of a prefill batch (q_len L > 0) is refused, none of its rows read or written, when its
+// rows do not lie inside the T rows of the call or its positions inside [0, 262144) (no sum that could
+// overflow is formed).
+inline __device__ bool rows_ok(const SeqRows& r, int qs, int L, int cs) {
+  return qs >= 0 && L <= r.T - qs && cs >= 0 && L <= kMaxPos && cs <= kMaxPos - L;
+}
+
 // A layer's paged cache and the head counts of the call: hkv KV heads in the cache (its page-head
 // blocks), hq query heads in the q and out rows. The full geometry has 32 / 16 (sliding) or 32 / 4
 // (global); a tensor-parallel rank slice has 32 / tp query heads and 16 / tp or max(1, 4 / tp) KV

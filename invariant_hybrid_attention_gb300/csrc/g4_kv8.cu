@@ -183,12 +183,6 @@ struct AppendArgs {
   int parts;   // warps per row
 };
 
-// Sequence b of a prefill batch is refused (none of its rows is read or written) when its rows do
-// not lie inside the T rows of the call or its positions inside [0, 262144).
-G4_DEV bool rows_ok(const SeqRows& r, int qs, int L, int cs) {
-  return qs >= 0 && L <= r.T - qs && cs >= 0 && L <= kMaxPos && cs <= kMaxPos - L;
-}
-
 // Bound by the latency of its loads (24 warps an SM, the ALU pipe 55% busy): the 4 x 4096 sliding rows take
 // 79 us (402 MB, 5.1 TB/s), the 2 x 8192 global ones 27 us (109 MB, 4 TB/s).
 // One warp per (row, share of the KV heads). The row's angles are computed once for its heads, in two-part

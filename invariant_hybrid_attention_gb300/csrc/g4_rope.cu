@@ -479,7 +479,8 @@ __device__ __forceinline__ void append_token(const __nv_bfloat16* k_row, const _
   append_token_cs<D, R, SHARED, NORM>(k_row, v_row, b, pos, c, cs, err, nm, wk, g_begin, g_end);
 }
 
-// One warp per row of the prefill batch; the owning sequence is found by a scan over B.
+// One warp per row of the prefill batch; the owning sequence is found by a scan over B (refused ones own
+// no row).
 // With q_out set, the row's query heads are also roped (declared bf16 cast) into q_out: the
 // attention kernel that follows reads its queries already rotated.
 template <int D, int R, bool SHARED, bool NORM>
@@ -498,21 +499,22 @@ __global__ void __launch_bounds__(256) append_prefill_kernel(const __nv_bfloat16
     bool mine = false;
     if (b < rows.B) {
       const int s = rows.q_start[b], L = rows.q_len[b];
-      mine = (L > 0 && r >= s && r - s < L);
+      if (L > 0) {
+        const bool ok = rows_ok(rows, s, L, rows.ctx_start[b]);
+        if (!ok && r == 0) set_error(err, kErrPos);
+        mine = ok && r >= s && r - s < L;
+      }
     }
     const unsigned m = __ballot_sync(0xffffffffu, mine);
-    if (m) {
-      owner = b0 + __ffs(m) - 1;
-      break;
-    }
+    if (m && owner < 0) owner = b0 + __ffs(m) - 1;
+    if (owner >= 0 && r != 0) break;   // row 0's warp looks at every sequence, for its error
   }
   if (owner < 0) return;
-  const long long pos64 = (long long)rows.ctx_start[owner] + (r - rows.q_start[owner]);   // no int overflow
-  if (pos64 < 0 || pos64 >= kMaxPos || (int)(pos64 >> 4) >= cache.max_pages) {
+  const int pos = rows.ctx_start[owner] + (r - rows.q_start[owner]);
+  if ((pos >> 4) >= cache.max_pages) {
     if (lane == 0) set_error(err, kErrPos);
     return;
   }
-  const int pos = (int)pos64;
   float2 cs[8];   // the row's angles, shared by its query heads and its key heads
   rope_cs_lane8<D, R>(tb, pos, cs);
   float wk[16];

@@ -3,8 +3,9 @@ import pytest
 import torch
 
 import invariant_hybrid_attention_gb300 as g4
-from invariant_hybrid_attention_gb300.paged import PagedKV8
+from invariant_hybrid_attention_gb300.paged import PagedKV, PagedKV8
 
+from gpu_cases import Norms
 from test_gpu_kv8 import Rows, Step, i32, make_layers, status_ok
 from test_gpu_tp import rank_heads
 
@@ -39,3 +40,104 @@ def test_decode_rank_slices_are_the_full_call_bit_for_bit(kind, tp, weights):
         g4.g4attn_kv8_decode(layer, None, q, None, None, i32(s.lens), cache.desc, r.table, out, ws, page_weights=w)
         status_ok()
         assert torch.equal(out, s.out[:, q0:q1]), (kind, tp, rank)
+
+
+# ---- refused sequences in staged calls ------------------------------------------------------------------
+
+# A refused sequence (q_start, q_len, ctx_start), listed before the valid one and overlapping its rows.
+REFUSED = {"past the rows": lambda T: (T - 9, 60, 0), "before the rows": lambda T: (-4, 60, 0),
+           "past the positions": lambda T: (0, 30, 262144 - 20), "negative positions": lambda T: (0, 30, -3)}
+
+
+class Overlap:
+    """One valid sequence, and a refused one listed before it."""
+
+    def __init__(self, kind, refused, normed, image):
+        self.r = r = Rows(kind, [70], [40], seed=103, spare=8)
+        self.weights = Norms(kind, 7) if normed else None   # (holds the device tensors)
+        self.norms = self.weights.arg if normed else None
+        bad = REFUSED[refused](r.T)
+        used = set(r.table[0].tolist())
+        spare = [p for p in range(r.plan.num_pages) if p not in used]
+        assert len(spare) >= 4
+        width = r.table.shape[1]
+        row = torch.tensor([spare[i % len(spare)] for i in range(width)], dtype=torch.int32, device="cuda")
+        self.table = torch.stack([row, r.table[0]]).contiguous()
+        self.args = [i32([x, y]) for x, y in zip(bad, (r.start[0], 70, 40))]
+        self.alone = r.row_args()
+        self.span = None
+        if image:
+            self.span = torch.zeros(r.T, 2, dtype=torch.int32, device="cuda")
+            self.span[r.start[0] + 5:r.start[0] + 50] = torch.tensor([45, 90], dtype=torch.int32, device="cuda")
+        self.q, self.k = r.pack(r.q), r.pack(r.k)
+        self.v = None if r.v is None else r.pack(r.v)
+        self.gap = torch.ones(r.T, dtype=torch.bool, device="cuda")
+        self.gap[r.start[0]:r.start[0] + 70] = False
+
+    def check(self, call, caches):
+        """call(rows, table, out, cache index): the valid sequence alone, then after the refused one."""
+        ref, out = torch.full_like(self.q, 5.0), torch.full_like(self.q, 5.0)
+        call(self.alone, self.r.table, ref, 0)
+        status_ok()
+        call(self.args, self.table, out, 1)
+        torch.cuda.synchronize()
+        assert g4.g4attn_status_sync() == g4.G4_ERR_DEVICE
+        assert torch.equal(out, ref)                              # gaps included: 5.0 in both
+        assert (out[self.gap] == 5.0).all()
+        for a, b in zip(*caches):
+            assert a is b is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("normed,image", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("refused", list(REFUSED))
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_staged_prefill_refuses_a_bad_sequence_and_serves_the_others(kind, refused, normed, image):
+    o = Overlap(kind, refused, normed, image)
+    o.r.append_history(o.norms)
+    caches = [PagedKV8(o.r.layer, o.r.plan.num_pages) for _ in range(2)]
+    scratch = [PagedKV(o.r.plan.num_pages, o.r.layer.n_kv_heads, o.r.layer.head_dim, kind == "global") for _ in range(2)]
+    for c in caches:
+        c.pages.copy_(o.r.cache.pages)
+
+    def call(rows, table, out, i):
+        g4.g4attn_kv8_prefill(o.r.layer, o.norms, o.q, o.k, o.v, *rows, caches[i].desc, table, scratch[i].desc, table, out,
+                              span=o.span)
+    o.check(call, [(c.pages, s.k, s.v, s.k_rot) for c, s in zip(caches, scratch)])
+
+
+@pytest.mark.parametrize("form", ["normed", "vision", "staged"])
+@pytest.mark.parametrize("refused", list(REFUSED))
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_staged_bf16_prefill_refuses_a_bad_sequence_and_serves_the_others(kind, refused, form):
+    o = Overlap(kind, refused, form != "staged", form == "vision")
+    layer, norms = o.r.layer, o.norms
+    caches = [PagedKV(o.r.plan.num_pages, layer.n_kv_heads, layer.head_dim, kind == "global") for _ in range(2)]
+    hist = (o.r.pack(o.r.k, True), None if o.v is None else o.r.pack(o.r.v, True), i32([0]), i32([40]), i32([0]))
+    for c in caches:
+        if norms is None:
+            g4.g4attn_kv_append(layer, *hist, c.desc, o.r.table)
+        else:
+            g4.g4attn_kv_append_normed(layer, norms, *hist, c.desc, o.r.table)
+
+    def call(rows, table, out, i):
+        c = caches[i].desc
+        if form == "normed":
+            g4.g4attn_prefill_normed(layer, norms, o.q, o.k, o.v, *rows, c, table, out)
+        elif form == "vision":
+            g4.g4attn_prefill_vision(layer, norms, o.q, o.k, o.v, *rows, o.span, c, table, out)
+        else:
+            g4.g4attn_prefill_stage(layer, o.q, o.k, o.v, *rows, c, table, out)
+            g4.g4attn_prefill_attend(layer, None, *rows, c, table, out)
+    o.check(call, [(c.k, c.v, c.k_rot) for c in caches])
+
+
+@pytest.mark.parametrize("refused", list(REFUSED))
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_normed_append_refuses_a_bad_sequence_whole(kind, refused):
+    o = Overlap(kind, refused, True, False)
+    layer = o.r.layer
+    caches = [PagedKV(o.r.plan.num_pages, layer.n_kv_heads, layer.head_dim, kind == "global") for _ in range(2)]
+
+    def call(rows, table, out, i):
+        g4.g4attn_kv_append_normed(layer, o.norms, o.k, o.v, *rows, caches[i].desc, table)
+    o.check(call, [(c.k, c.v, c.k_rot) for c in caches])
