@@ -434,8 +434,8 @@ size_t g4attn_kv8_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, i
  *                  `window` held ones on sliding layers.
  *   page_weights   float [B][max_pages], device, or NULL; global layers only (G4_ERR_UNSUPPORTED else):
  *                  page_weights[b][i] += the softmax weight of held page i's keys, summed over the
- *                  query heads (a step adds n_q_heads over a sequence's pages). Entries past the held
- *                  pages are not touched. Calls that share a buffer must be ordered.
+ *                  query heads (a step adds n_q_heads over a sequence's pages; a chunk with a page outside
+ *                  the pool, or whose wait ran out, adds nothing). Entries past the held pages are not touched. Calls that share a buffer must be ordered.
  * The query is turned and cast to bf16; the softmax weights are cast to fp16 for the value product. out may be
  * q. Calls that may run at the same time need workspaces of their own; its contents on entry do not
  * matter. A key that holds a NaN vector makes the rows of its head that see it NaN, and the page weights

@@ -525,10 +525,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
       red_m2[warp][2 * cq + j] = m2[j];
     }
   }
-  __syncthreads();   // every stage has been read: reuse the ring for the warp merge
+  const bool cut = __syncthreads_or(n < mine);   // every stage has been read: reuse the ring for the warp merge
   float* page_out = PAGES ? p.ws_page + (((size_t)b * HKV + g) * p.cache.max_pages + pg0) * 8 : nullptr;
-  if (void_chunk) {   // a page outside the pool: nothing but a state that adds nothing
-    if (threadIdx.x == 0) set_error(p.err, kErrPage);
+  if (void_chunk || cut) {   // a page outside the pool, or a wait that ran out: a state that adds nothing
+    if (threadIdx.x == 0 && void_chunk) set_error(p.err, kErrPage);
     if (!PAGES && p.out) {
       zero_heads<D>(p.out + ((size_t)b * p.cache.hq + (size_t)G * g) * D, G);
       return;

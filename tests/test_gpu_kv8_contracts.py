@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import invariant_hybrid_attention_gb300 as g4
+from invariant_hybrid_attention_gb300 import inputs as gi
 from invariant_hybrid_attention_gb300.paged import PagedKV, PagedKV8
 
 from gpu_cases import Norms
@@ -141,3 +142,41 @@ def test_normed_append_refuses_a_bad_sequence_whole(kind, refused):
     def call(rows, table, out, i):
         g4.g4attn_kv_append_normed(layer, o.norms, o.k, o.v, *rows, caches[i].desc, table)
     o.check(call, [(c.k, c.v, c.k_rot) for c in caches])
+
+
+# ---- a wait that runs out ---------------------------------------------------------------------------------
+
+def test_decode_wait_that_runs_out_leaves_finite_page_weights():
+    """64 requests of 4096 keys with the limit at 0: some waits give up. The accumulators, which live on over steps,
+    get what was computed or nothing: at most one unit per query head and request."""
+    layer, _ = make_layers("global")
+    B, width = 64, 256
+    cache = PagedKV8(layer, B * width, fill=None)
+    cache.pages.random_(100, 140)                     # exponents too: steps around 2^-13
+    table = torch.arange(B * width, dtype=torch.int32, device="cuda").view(B, width)
+    q = gi.bf16_normal((B, 32, 512), 3).cuda()
+    ws = torch.empty(g4.g4attn_kv8_decode_workspace_bytes(layer, B, width, True), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, float("nan"))
+
+    def run(w):
+        g4.g4attn_kv8_decode(layer, None, q, None, None, i32([16 * width] * B), cache.desc, table, out, ws, page_weights=w)
+        torch.cuda.synchronize()
+        return g4.g4attn_status_sync()
+    ref = torch.zeros(B, width, device="cuda")
+    assert run(ref) == g4.G4_OK
+    good = out.clone()
+    for _ in range(5):
+        w = torch.ones(B, width, device="cuda")
+        ws.fill_(255)                                 # the next kernel's shared memory is not the last call's
+        torch.randn(1 << 24, device="cuda").sort()
+        g4.g4attn_set_wait_limit_ns(0)
+        try:
+            st = run(w)
+        finally:
+            g4.g4attn_set_wait_limit_ns(g4.DEFAULT_WAIT_LIMIT_NS)
+        assert st == g4.G4_ERR_TIMEOUT, g4.status_string(st)
+        assert w.isfinite().all() and (w >= 1).all() and out.isfinite().all()
+        # a request's shares sum to its heads (n_q_heads, fp32 sums of 256 pages: 2^-16), or to less
+        assert ((w - 1).double().sum(1) <= 32 * (1 + 2.0 ** -16)).all()
+    again = torch.zeros(B, width, device="cuda")
+    assert run(again) == g4.G4_OK and torch.equal(again, ref) and torch.equal(out, good)
