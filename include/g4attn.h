@@ -383,6 +383,9 @@ size_t g4attn_kv8_page_bytes(const g4attn_layer* layer);
 
 /* g4attn_kv_append_normed into an 8-bit cache (the RFC has no counterpart of it): writes the
  * rows' K' and V, or S and its turned columns. Row conventions and errors as there; norms may be NULL.
+ * A row's RoPE position is its held index. So a sequence that lost pages (g4attn_evict_pages), whose
+ * positions run ahead of its held keys, is not continued by this call or by g4attn_kv8_prefill, which
+ * would turn its rows too little without an error, but token by token by g4attn_kv8_decode with pos.
  * A sequence whose rows do not lie inside [0, T), or whose positions do not lie inside [0, 262144), is
  * refused on the device (G4_ERR_DEVICE), and so is each row whose page is not in the table or the pool. */
 g4_status g4attn_kv8_append(const g4attn_layer* layer, const g4attn_norms* norms, const void* k, const void* v,
@@ -411,7 +414,9 @@ g4_status g4attn_kv8_unpack(const g4attn_layer* layer, const int32_t* key_begin,
  * them in its page). norms and span may be NULL. A row's output does not depend on the batch around it or
  * on the chunks. Other arguments and errors as g4attn_prefill_vision; scratch_table: int32
  * [B][max_pages], the scratch page of each logical page a row of sequence b sees, distinct between
- * sequences. */
+ * sequences. RoPE positions as g4attn_kv8_append: not for sequences that lost pages. The attention
+ * casts the softmax weights to bf16 and forms the query's angles and norm as the bf16 prefill does, where
+ * g4attn_kv8_decode casts them to fp16: the two agree to those roundings, not to the bit. */
 g4_status g4attn_kv8_prefill(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k,
                              const void* v, int32_t T, const int32_t* q_start, const int32_t* q_len,
                              const int32_t* ctx_start, int32_t B, const int32_t* span, const g4attn_cache8* cache,
@@ -449,7 +454,8 @@ g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms
  * RFC). Sequence b holds n = ceil(seq_len[b] / 16) pages. When n > keep_pages, the n - keep_pages lightest
  * of its evictable pages leave: all but the first first_pages and the last last_pages (first_pages >= 0,
  * last_pages >= 1, first_pages + last_pages <= keep_pages). Of equal weights the lower index leaves
- * first; a NaN counts as the heaviest. No key moves: the table is closed up, in order.
+ * first; a NaN counts as the heaviest. No key moves: the table is closed up, in order. From then on the
+ * sequence's positions run ahead of its held keys: continue it by g4attn_kv8_decode with pos alone.
  *   out_seq_len [B]             seq_len - 16 per evicted page
  *   out_table, out_weights [B][max_pages]  the kept pages and their weights, then -1 and 0
  *   freed [B][max_pages], n_freed [B]      the evicted physical pages in their order, then -1

@@ -395,7 +395,8 @@ def g4attn_kv8_page_bytes(layer) -> int:
 
 
 def g4attn_kv8_append(layer, norms, k, v, q_start, q_len, ctx_start, cache: g4attn_cache8, page_table, stream=None):
-    """g4attn_kv_append_normed into an 8-bit cache; norms may be None."""
+    """g4attn_kv_append_normed into an 8-bit cache; norms may be None. Rows are turned by their held index: a
+    sequence that lost pages is continued by g4attn_kv8_decode with pos instead."""
     bf, i32, _, _, _ = _names or _torch_names()
     T, B, width = k.shape[0], q_start.shape[0], page_table.shape[-1]
     kv, rows = (T, layer.n_kv_heads, layer.head_dim), (B,)
@@ -422,7 +423,8 @@ def g4attn_kv8_unpack(layer, key_begin, key_end, cache: g4attn_cache8, page_tabl
 
 def g4attn_kv8_prefill(layer, norms, q, k, v, q_start, q_len, ctx_start, cache: g4attn_cache8, page_table,
                        scratch: g4attn_cache, scratch_table, out, span=None, stream=None):
-    """A prefill (or chunk) over an 8-bit cache; scratch: a bf16 cache for the keys its rows see."""
+    """A prefill (or chunk) over an 8-bit cache; scratch: a bf16 cache for the keys its rows see. Not for
+    sequences that lost pages (see g4attn_kv8_append)."""
     bf, i32, _, _, _ = _names or _torch_names()
     T, B, width = q.shape[0], q_start.shape[0], page_table.shape[-1]
     qo, kv = (T, layer.n_q_heads, layer.head_dim), (T, layer.n_kv_heads, layer.head_dim)
@@ -463,7 +465,8 @@ def g4attn_kv8_decode(layer, norms, q, k_new, v_new, seq_len, cache: g4attn_cach
 
 def g4attn_evict_pages(seq_len, page_table, page_weights, keep_pages: int, first_pages: int, last_pages: int,
                        out_seq_len, out_table, out_weights, freed, n_freed, stream=None):
-    """Evicts each sequence's lightest pages down to keep_pages; the out_ tensors may be the inputs."""
+    """Evicts each sequence's lightest pages down to keep_pages; the out_ tensors may be the inputs. The sequence
+    goes on by g4attn_kv8_decode with pos."""
     _, i32, f32, _, _ = _names or _torch_names()
     B, width = seq_len.shape[0], page_table.shape[-1]
     rows, table = (B,), (B, width)
