@@ -1,4 +1,5 @@
 """Promises of the header that the 8-bit cache's calls share with the bf16 ones, held to the bit."""
+import numpy as np
 import pytest
 import torch
 
@@ -180,3 +181,123 @@ def test_decode_wait_that_runs_out_leaves_finite_page_weights():
         assert ((w - 1).double().sum(1) <= 32 * (1 + 2.0 ** -16)).all()
     again = torch.zeros(B, width, device="cuda")
     assert run(again) == g4.G4_OK and torch.equal(again, ref) and torch.equal(out, good)
+
+
+# ---- image spans --------------------------------------------------------------------------------------------
+
+def agree(x, axis_max):
+    """Whether the 8-bit and the bf16 cast of x give one number, both away from their borders by 2% of a step
+    (axis_max: largest |x| of the stored vector)."""
+    def near(y):
+        return np.abs(np.abs(y - np.floor(y)) - 0.5) > 0.02
+    top = np.floor(np.log2(np.maximum(axis_max, 1e-30)))
+    inside = (axis_max / 2.0 ** top > 1.002) & (axis_max / 2.0 ** top < 127.4 / 64)
+    a = x / 2.0 ** (top - 6)
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 1e-30))) - 7)
+    b = x / step
+    return inside & near(a) & near(b) & (np.rint(a) * 2.0 ** (top - 6) == np.rint(b) * step)
+
+
+def exact_rows(r, norms, seed):
+    """Fills a Rows batch with rows whose stored K' and V (or S and its turned columns) are the same numbers in an
+    8-bit and in a bf16 cache: values of 7 bits, or signs whose common normed size rounds alike, and keys with one
+    turning pair per head, searched so that both casts of its turned value agree."""
+    d, pairs = r.layer.head_dim, 64 if r.kind == "global" else 128
+    theta = 1e6 if r.kind == "global" else 1e4
+    rng = np.random.default_rng(seed)
+    plain = np.setdiff1d(np.arange(d), np.concatenate([np.arange(pairs), np.arange(d // 2, d // 2 + pairs)]))
+    w = np.ones(d) if norms is None else norms.oracle.k_weight
+    fitting = [m for m in range(20, d - 2 * pairs if r.kind == "global" else d)
+               if agree(np.array((m / d + 1e-6) ** -0.5), np.array((m / d + 1e-6) ** -0.5))]
+    for b, x in enumerate(r.k):
+        n, h = x.shape[:2]
+        v = np.zeros((n, h, d))
+        size = np.ones((n, h))
+        if norms is None:
+            v[:] = rng.integers(-127, 128, v.shape) / 64.0
+            v[..., 3 if r.kind == "sliding" else plain[0]] = 1.5
+        else:
+            columns = plain if r.kind == "global" else np.arange(d)
+            m = rng.choice(fitting, (n, h))
+            size = (m / d + 1e-6) ** -0.5
+            order = rng.random((n, h, len(columns))).argsort(-1).argsort(-1)
+            count = m - (2 if r.kind == "global" else 0)      # a global row's pair is two of the m
+            v[..., columns] = np.where(order < count[..., None], rng.choice([-1.0, 1.0], order.shape), 0.0)
+        # candidates: a pair t and its two columns
+        c = 160
+        t = rng.integers(0, pairs, (n, h, c))
+        if norms is not None and r.kind == "global":
+            lo, hi = (rng.choice([-1.0, 1.0], t.shape) for _ in range(2))
+            k_lo, k_hi = lo * size[..., None], hi * size[..., None]
+        else:
+            lo, hi = (rng.integers(-100, 101, t.shape) / 64.0 for _ in range(2))
+            k_lo, k_hi = lo, hi
+            if norms is not None:
+                root = np.sqrt((lo * lo + hi * hi) / d + 1e-6)
+                k_lo, k_hi = lo / root, hi / root
+        k_lo, k_hi = k_lo * w[t], k_hi * w[t + d // 2]
+        angle = np.arange(n)[:, None, None] * theta ** (-2.0 * t / d)
+        u = np.stack([k_lo * np.cos(angle) - k_hi * np.sin(angle), k_hi * np.cos(angle) + k_lo * np.sin(angle)])
+        ok = agree(u, np.abs(u).max(0)).all(0)
+        pick = ok.argmax(-1)[..., None]
+        found = np.take_along_axis(ok, pick, -1)[..., 0]
+        t, lo, hi = (np.take_along_axis(y, pick, -1)[..., 0] for y in (t, lo, hi))
+        key = np.zeros((n, h, d)) if r.kind == "sliding" else v
+        if r.kind == "global":
+            key[..., np.setdiff1d(np.arange(d), plain)] = 0.0
+        i, j = np.nonzero(found)
+        key[i, j, t[i, j]], key[i, j, t[i, j] + d // 2] = lo[i, j], hi[i, j]
+        if norms is not None and r.kind == "global":          # a row without its pair has two ones less
+            for i, j in zip(*np.nonzero(~found)):
+                rest = np.nonzero(v[i, j] == 0)[0]
+                rest = rest[np.isin(rest, plain)][:2]
+                v[i, j, rest] = 1.0
+        assert found.mean() > 0.9
+        x.copy_(torch.tensor(key).bfloat16())
+        if r.v is not None:
+            r.v[b].copy_(torch.tensor(v).bfloat16())
+
+
+@pytest.mark.parametrize("normed", [False, True])
+@pytest.mark.parametrize("kind,window", [("sliding", 1024), ("sliding", 16), ("global", 0)])
+def test_prefill_with_image_spans_is_the_bf16_call_bit_for_bit(kind, window, normed):
+    """Where both caches hold the same numbers, the two prefills give the same bits: one key more or less at an
+    image's end, or a stale key before a window, would show. Images inside a chunk, past a window, and begun before
+    the chunk."""
+    norms = Norms(kind, 12) if normed else None
+    arg = None if norms is None else norms.arg
+    r = Rows(kind, [150, 1300, 90, 40], [30, 0, 70, 333], seed=104, gap=1, norms=norms, window=window or 1024)
+    exact_rows(r, norms, 5)
+    images = [(50, 140), (20, 1200), (33, 71), (0, 0)]
+    span = torch.full((r.T, 2), -1, dtype=torch.int32)
+    for b, (s0, s1) in enumerate(images):
+        first, n = r.start[b], r.rows[b]
+        span[first:first + n] = 0
+        lo = max(s0, r.ctx[b])
+        span[first + lo - r.ctx[b]:first + s1 - r.ctx[b]] = torch.tensor([s0, s1], dtype=torch.int32)
+    span = span.cuda()
+    r.append_history(arg)
+    bf = PagedKV(r.plan.num_pages, r.layer.n_kv_heads, r.layer.head_dim, kind == "global")
+    starts = [sum(r.ctx[:b]) for b in range(4)]
+    hist = (r.pack(r.k, True), None if r.v is None else r.pack(r.v, True), i32(starts), i32(r.ctx), i32([0] * 4))
+    if arg is None:
+        g4.g4attn_kv_append(r.layer, *hist, bf.desc, r.table)
+    else:
+        g4.g4attn_kv_append_normed(r.layer, arg, *hist, bf.desc, r.table)
+    q, k, v = r.pack(r.q), r.pack(r.k), None if r.v is None else r.pack(r.v)
+    want = torch.full_like(q, 5.0)
+    g4.g4attn_prefill_vision(r.layer, arg, q, k, v, *r.row_args(), span, bf.desc, r.table, want)
+    status_ok()
+    scratch = PagedKV(r.plan.num_pages, r.layer.n_kv_heads, r.layer.head_dim, kind == "global")
+    got = torch.full_like(q, 5.0)
+    g4.g4attn_kv8_prefill(r.layer, arg, q, k, v, *r.row_args(), r.cache.desc, r.table, scratch.desc, r.table, got, span=span)
+    status_ok()
+    # both caches hold the same numbers (the read-back of every key against the bf16 pages)
+    everything = PagedKV(r.plan.num_pages, r.layer.n_kv_heads, r.layer.head_dim, kind == "global")
+    lens = [n + c for n, c in r.pairs()]
+    g4.g4attn_kv8_unpack(r.layer, i32([0] * 4), i32(lens), r.cache.desc, r.table, everything.desc, r.table)
+    status_ok()
+    for a, b in ((everything.k, bf.k), (everything.v, bf.v), (everything.k_rot, bf.k_rot)):
+        if a is not None:
+            assert torch.equal(a.nan_to_num(9.0), b.nan_to_num(9.0))
+    assert got.isfinite().all() and torch.equal(got, want)
