@@ -47,10 +47,14 @@ class g4attn_norms(ctypes.Structure):
 class g4attn_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_rot", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+    tensors = None   # make_cache: what k, v and k_rot point into
+    room = None      # see _room16
 
 
 class g4attn_cache8(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+    tensor = None    # make_cache8: what pages points into (None: a raw address)
+    room = None      # its bytes and its device
 
 
 class G4Error(RuntimeError):
@@ -134,7 +138,9 @@ def global_layer(softmax_scale: Optional[float] = None, tp: int = 1) -> g4attn_l
 
 
 def make_cache(k, v, num_pages: int, k_rot=None) -> g4attn_cache:
-    return g4attn_cache(_ptr(k), _ptr(v), _ptr(k_rot), int(num_pages), PAGE_SIZE)
+    cache = g4attn_cache(_ptr(k), _ptr(v), _ptr(k_rot), int(num_pages), PAGE_SIZE)
+    cache.tensors = (k, v, k_rot)
+    return cache
 
 
 def _ptr(t) -> Optional[int]:
@@ -340,8 +346,9 @@ def g4attn_merge_partials(layer, o_parts, ml_parts, q_start, q_len, out, stream=
 
 # ---- the 8-bit paged cache ----------------------------------------------------------------------------
 # The kernels take dense tensors of one type on the current device; these calls check that, since a
-# raw pointer cannot say otherwise. A small step's kernels run for 7 us, so the checks are one pass over the
-# arguments, with torch's names looked up once.
+# raw pointer cannot say otherwise, and that a cache's tensors hold the pages that it is said to have. A small
+# step's kernels run for 6 us, so the checks are one pass over the arguments, with torch's names looked up once,
+# and what a cache descriptor points into is looked at once per descriptor.
 
 _names = None   # (bfloat16, int32, float32, the current device, a device's current raw stream)
 
@@ -354,16 +361,56 @@ def _torch_names():
 
 
 def make_cache8(pages, num_pages: int) -> g4attn_cache8:
-    return g4attn_cache8(_ptr(pages), int(num_pages), PAGE_SIZE)
+    """pages: a dense tensor (or a raw address, which nothing checks) of num_pages pages."""
+    cache = g4attn_cache8(_ptr(pages), int(num_pages), PAGE_SIZE)
+    if not isinstance(pages, int):
+        if not pages.is_contiguous():
+            raise ValueError("make_cache8: pages must be dense")
+        cache.tensor, cache.room = pages, (pages.nbytes, pages.get_device())
+    return cache
 
 
-def _pointers(what: str, stream, specs):
+_BLOCK8 = {256: 8224, 512: 10272}   # bytes of a page and KV head of an 8-bit cache, by head_dim
+
+
+def _room16(what: str, cache: g4attn_cache):
+    """Bytes that k and v each hold at least, those of k_rot, and the one device of all three (-2: several, None: raw
+    addresses alone); kept in the descriptor."""
+    given = [t for t in cache.tensors or () if t is not None and not isinstance(t, int)]
+    if not all(t.is_contiguous() for t in given):
+        raise ValueError(f"{what}: the bf16 cache's tensors must be dense")
+    sizes = [1 << 62 if t is None or isinstance(t, int) else t.nbytes for t in cache.tensors or (None,) * 3]
+    at = {t.get_device() for t in given}
+    cache.room = (min(sizes[0], sizes[1]), sizes[2], None if not at else at.pop() if len(at) == 1 else -2)
+    return cache.room
+
+
+def _refuse_pool(what: str, name: str, room, need, at, here: int):
+    if any(n > r for n, r in zip(need, room)):
+        raise ValueError(f"{what}: {name} has {room} bytes, its pages take {need}")
+    place = {-1: "the CPU", -2: "several devices"}.get(at, f"cuda:{at}")
+    raise ValueError(f"{what}: {name} is on {place}, not on the current CUDA device")
+
+
+def _pointers(what: str, stream, specs, layer=None, cache=None, bf16_cache=None):
     """The addresses of a call's tensors, given as (name, tensor, dtype, shape), and of its stream (None: the
-    current one). None and raw addresses pass unchecked; the first one is a tensor."""
+    current one). None and raw addresses pass unchecked; the first one is a tensor. cache, bf16_cache: descriptors
+    whose tensors have to hold their pages of the layer's heads, on the same device."""
     _, _, _, device, raw_stream = _names
     here = specs[0][1].get_device()
     if here >= 0:
         here = device()
+    if cache is not None and cache.room is not None:
+        room, at = cache.room
+        need = cache.num_pages * layer.n_kv_heads * _BLOCK8.get(layer.head_dim, 0)
+        if need > room or (at != here and here >= 0):
+            _refuse_pool(what, "the 8-bit cache", (room,), (need,), at, here)
+    if bf16_cache is not None:
+        room, rot_room, at = bf16_cache.room or _room16(what, bf16_cache)
+        blocks = bf16_cache.num_pages * layer.n_kv_heads
+        need = blocks * 32 * layer.head_dim
+        if need > room or blocks * 4096 > rot_room or (at != here and here >= 0 and at is not None):
+            _refuse_pool(what, "the bf16 cache", (room, rot_room), (need, blocks * 4096), at, here)
     out = []
     for name, t, dtype, shape in specs:
         if t is None or t.__class__ is int:
@@ -402,7 +449,8 @@ def g4attn_kv8_append(layer, norms, k, v, q_start, q_len, ctx_start, cache: g4at
     kv, rows = (T, layer.n_kv_heads, layer.head_dim), (B,)
     k, v, q_start, q_len, ctx_start, page_table, stream = _pointers("g4attn_kv8_append", stream, (
         ("k", k, bf, kv), ("v", v, bf, kv), ("q_start", q_start, i32, rows), ("q_len", q_len, i32, rows),
-        ("ctx_start", ctx_start, i32, rows), ("page_table", page_table, i32, (B, width))))
+        ("ctx_start", ctx_start, i32, rows), ("page_table", page_table, i32, (B, width))),
+        layer, cache)
     _check((_lib or load()).g4attn_kv8_append(ctypes.byref(layer), _opt(norms), k, v, T, q_start, q_len, ctx_start, B,
                                               ctypes.byref(cache), page_table, width, stream), "g4attn_kv8_append")
 
@@ -415,7 +463,7 @@ def g4attn_kv8_unpack(layer, key_begin, key_end, cache: g4attn_cache8, page_tabl
     rows, table = (B,), (B, width)
     key_begin, key_end, page_table, out_table, stream = _pointers("g4attn_kv8_unpack", stream, (
         ("key_begin", key_begin, i32, rows), ("key_end", key_end, i32, rows), ("page_table", page_table, i32, table),
-        ("out_table", out_table, i32, table)))
+        ("out_table", out_table, i32, table)), layer, cache, out)
     _check((_lib or load()).g4attn_kv8_unpack(ctypes.byref(layer), key_begin, key_end, B, ctypes.byref(cache),
                                               page_table, ctypes.byref(out), out_table, width, stream),
            "g4attn_kv8_unpack")
@@ -433,7 +481,8 @@ def g4attn_kv8_prefill(layer, norms, q, k, v, q_start, q_len, ctx_start, cache: 
         "g4attn_kv8_prefill", stream, (
             ("q", q, bf, qo), ("k", k, bf, kv), ("v", v, bf, kv), ("q_start", q_start, i32, rows),
             ("q_len", q_len, i32, rows), ("ctx_start", ctx_start, i32, rows), ("span", span, i32, (T, 2)),
-            ("page_table", page_table, i32, table), ("scratch_table", scratch_table, i32, table), ("out", out, bf, qo)))
+            ("page_table", page_table, i32, table), ("scratch_table", scratch_table, i32, table), ("out", out, bf, qo)),
+        layer, cache, scratch)
     _check((_lib or load()).g4attn_kv8_prefill(ctypes.byref(layer), _opt(norms), qp, k, v, T, q_start, q_len, ctx_start,
                                                B, span, ctypes.byref(cache), page_table, ctypes.byref(scratch),
                                                scratch_table, width, op, stream), "g4attn_kv8_prefill")
@@ -456,7 +505,8 @@ def g4attn_kv8_decode(layer, norms, q, k_new, v_new, seq_len, cache: g4attn_cach
     q, k_new, v_new, seq_len, pos, page_table, page_weights, op, work, stream = _pointers("g4attn_kv8_decode", stream, (
         ("q", q, bf, qo), ("k_new", k_new, bf, kv), ("v_new", v_new, bf, kv), ("seq_len", seq_len, i32, rows),
         ("pos", pos, i32, rows), ("page_table", page_table, i32, table), ("page_weights", page_weights, f32, table),
-        ("out", out, bf, qo), ("workspace", workspace, workspace.dtype, workspace.shape)))
+        ("out", out, bf, qo), ("workspace", workspace, workspace.dtype, workspace.shape)),
+        layer, cache)
     _check((_lib or load()).g4attn_kv8_decode(ctypes.byref(layer), _opt(norms), q, k_new, v_new, seq_len, pos, B,
                                               ctypes.byref(cache), page_table, width, page_weights, op, work,
                                               workspace.nbytes, stream), "g4attn_kv8_decode")

@@ -301,3 +301,22 @@ def test_prefill_with_image_spans_is_the_bf16_call_bit_for_bit(kind, window, nor
         if a is not None:
             assert torch.equal(a.nan_to_num(9.0), b.nan_to_num(9.0))
     assert got.isfinite().all() and torch.equal(got, want)
+
+
+# ---- caches elsewhere ---------------------------------------------------------------------------------------
+
+def test_a_cache_or_scratch_on_another_device_is_refused():
+    r = Rows("global", [40], seed=105, gap=0)
+    s = Step(r)
+    elsewhere = PagedKV8(r.layer, r.plan.num_pages, device="cpu")
+    with pytest.raises(ValueError, match="the 8-bit cache is on the CPU"):
+        g4.g4attn_kv8_decode(r.layer, None, s.q, None, None, i32(s.lens), elsewhere.desc, r.table, s.out, s.ws)
+    with pytest.raises(ValueError, match="the 8-bit cache is on the CPU"):
+        g4.g4attn_kv8_append(r.layer, None, r.pack(r.k), None, *r.row_args(), elsewhere.desc, r.table)
+    scratch = PagedKV(r.plan.num_pages, 4, 512, True, device="cpu")
+    q = r.pack(r.q)
+    with pytest.raises(ValueError, match="the bf16 cache is on the CPU"):
+        g4.g4attn_kv8_prefill(r.layer, None, q, r.pack(r.k), None, *r.row_args(), r.cache.desc, r.table, scratch.desc,
+                              r.table, q)
+    with pytest.raises(ValueError, match="the bf16 cache is on the CPU"):
+        g4.g4attn_kv8_unpack(r.layer, i32([0]), i32([40]), r.cache.desc, r.table, scratch.desc, r.table)
