@@ -37,6 +37,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "g4_kv8.cuh"
 
 namespace g4 {
@@ -799,7 +801,7 @@ cudaError_t finish(const Decode8Params& p, int chunk, void* out, float* page_wei
 
 template <bool GLOBAL, bool PAGES>
 cudaError_t launch(const Decode8Params& p, cudaStream_t s) {
-  static bool done[64] = {};
+  static std::atomic<bool> done[64];   // per device; two first calls at once both set the attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
