@@ -31,8 +31,9 @@
  *
  * Memory. Every tensor is a device buffer owned by the caller. The library allocates no
  * device memory: its only device-side state is static (the RoPE cos/sin tables, filled once
- * per device on the first call, one 32-bit error word, and the scratch buffer of
- * g4attn_decode_static). All calls are stream-ordered
+ * per device on the first call, which must come before any stream capture; the finer ones of the
+ * 8-bit calls, filled by each layer kind's first of them, captured or not; one 32-bit error word, and
+ * the scratch buffer of g4attn_decode_static). All calls are stream-ordered
  * on `stream` (a cudaStream_t; NULL = the legacy default stream) and never synchronise,
  * except g4attn_status_sync.
  *

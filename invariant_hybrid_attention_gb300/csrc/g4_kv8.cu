@@ -2,6 +2,8 @@
 // and the cast).
 #include <math.h>
 
+#include <atomic>
+#include <mutex>
 #include <vector>
 
 #include "g4_kv8.cuh"
@@ -12,48 +14,84 @@ static __device__ float4 g_kv8_coarse_sliding[kRopeCoarse * kSlidingR];
 static __device__ float4 g_kv8_fine_sliding[256 * kSlidingR];
 static __device__ float4 g_kv8_coarse_global[kRopeCoarse * kGlobalR];
 static __device__ float4 g_kv8_fine_global[256 * kGlobalR];
-static Kv8Angles g_angles[64][2];   // per device and layer kind; written once, by the device's first call
 
-// Fills the tables of the current device (computed in fp64 on the host; no exception leaves).
-cudaError_t upload_kv8_angles() {
-  auto fill = [](const void* symbol, int entries, double step, int D, int R, double theta) {
-    std::vector<float4> h((size_t)entries * R);
-    for (int t = 0; t < R; ++t) {
-      const double f = pow(theta, -2.0 * t / (double)D);
-      for (int i = 0; i < entries; ++i) {
-        const double c = cos((step * i) * f), s = sin((step * i) * f);
-        const float ch = (float)c, sh = (float)s;
-        h[(size_t)i * R + t] = make_float4(ch, sh, (float)(c - ch), (float)(s - sh));
-      }
+namespace {
+
+constexpr int kAngleDevices = 64;
+std::mutex g_angles_mutex;
+std::atomic<bool> g_angles_ready[kAngleDevices][2];   // per device and layer kind
+Kv8Angles g_angles[kAngleDevices][2];
+
+// The table of angles (step i) f_t, i < entries, in two fp32 parts (computed in fp64).
+std::vector<float4> angle_table(int entries, double step, int D, int R, double theta) {
+  std::vector<float4> h((size_t)entries * R);
+  for (int t = 0; t < R; ++t) {
+    const double f = pow(theta, -2.0 * t / (double)D);
+    for (int i = 0; i < entries; ++i) {
+      const double c = cos((step * i) * f), s = sin((step * i) * f);
+      const float ch = (float)c, sh = (float)s;
+      h[(size_t)i * R + t] = make_float4(ch, sh, (float)(c - ch), (float)(s - sh));
     }
-    return cudaMemcpyToSymbol(symbol, h.data(), h.size() * sizeof(float4));
-  };
-  try {
-    cudaError_t e;
-    int dev = 0;
-    void* at[4];
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if ((e = fill(g_kv8_coarse_sliding, kRopeCoarse, 256.0, kSlidingD, kSlidingR, 1.0e4)) != cudaSuccess) return e;
-    if ((e = fill(g_kv8_fine_sliding, 256, 1.0, kSlidingD, kSlidingR, 1.0e4)) != cudaSuccess) return e;
-    if ((e = fill(g_kv8_coarse_global, kRopeCoarse, 256.0, kGlobalD, kGlobalR, 1.0e6)) != cudaSuccess) return e;
-    if ((e = fill(g_kv8_fine_global, 256, 1.0, kGlobalD, kGlobalR, 1.0e6)) != cudaSuccess) return e;
-    if ((e = cudaGetSymbolAddress(&at[0], g_kv8_coarse_sliding)) != cudaSuccess) return e;
-    if ((e = cudaGetSymbolAddress(&at[1], g_kv8_fine_sliding)) != cudaSuccess) return e;
-    if ((e = cudaGetSymbolAddress(&at[2], g_kv8_coarse_global)) != cudaSuccess) return e;
-    if ((e = cudaGetSymbolAddress(&at[3], g_kv8_fine_global)) != cudaSuccess) return e;
-    for (int k = 0; k < 2; ++k) g_angles[dev][k] = Kv8Angles{(const float4*)at[2 * k], (const float4*)at[2 * k + 1]};
-    return cudaSuccess;
+  }
+  return h;
+}
+
+// Copies a layer kind's tables to the current device, on a stream of its own: the call that needs them may
+// be part of a capture, which must neither record the copy nor be broken by it.
+cudaError_t copy_tables(const void* coarse_symbol, const std::vector<float4>& coarse, const void* fine_symbol,
+                        const std::vector<float4>& fine) {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return e;
+  cudaStream_t s = nullptr;
+  e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e == cudaSuccess) {
+    e = cudaMemcpyToSymbolAsync(coarse_symbol, coarse.data(), coarse.size() * sizeof(float4), 0,
+                                cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess)
+      e = cudaMemcpyToSymbolAsync(fine_symbol, fine.data(), fine.size() * sizeof(float4), 0, cudaMemcpyHostToDevice, s);
+    const cudaError_t done = cudaStreamSynchronize(s);   // before the host tables go
+    if (e == cudaSuccess) e = done;
+    cudaStreamDestroy(s);
+  }
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return e;
+}
+
+cudaError_t upload_angles(int dev, bool global) {
+  const void* coarse = global ? (const void*)g_kv8_coarse_global : (const void*)g_kv8_coarse_sliding;
+  const void* fine = global ? (const void*)g_kv8_fine_global : (const void*)g_kv8_fine_sliding;
+  const int D = global ? kGlobalD : kSlidingD, R = global ? kGlobalR : kSlidingR;
+  const double theta = global ? 1.0e6 : 1.0e4;
+  try {   // no exception leaves a C entry point
+    const cudaError_t e = copy_tables(coarse, angle_table(kRopeCoarse, 256.0, D, R, theta), fine,
+                                      angle_table(256, 1.0, D, R, theta));
+    if (e != cudaSuccess) return e;
   } catch (...) {
     return cudaErrorMemoryAllocation;
   }
+  void *c = nullptr, *f = nullptr;
+  cudaError_t e;
+  if ((e = cudaGetSymbolAddress(&c, coarse)) != cudaSuccess) return e;
+  if ((e = cudaGetSymbolAddress(&f, fine)) != cudaSuccess) return e;
+  g_angles[dev][global] = Kv8Angles{(const float4*)c, (const float4*)f};
+  return cudaSuccess;
 }
+
+}  // namespace
 
 cudaError_t kv8_angles(bool global, Kv8Angles* out) {
   int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !g_angles[dev][global].coarse) return cudaErrorInvalidDevice;
+  if (dev < 0 || dev >= kAngleDevices) return cudaErrorInvalidDevice;
+  if (!g_angles_ready[dev][global].load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(g_angles_mutex);
+    if (!g_angles_ready[dev][global].load(std::memory_order_relaxed)) {
+      if ((e = upload_angles(dev, global)) != cudaSuccess) return e;
+      g_angles_ready[dev][global].store(true, std::memory_order_release);
+    }
+  }
   *out = g_angles[dev][global];
   return cudaSuccess;
 }

@@ -79,14 +79,13 @@ G4_DEV uint2 kv8_codes(const float (&x)[8], uint32_t biased) {
 
 // ---- angles ------------------------------------------------------------------------------------------
 // Tables of (cos, sin) in two fp32 parts (cos, sin, and what their rounding left), entry-major: coarse[c][t]
-// of 256 c f_t, fine[a][t] of a f_t, 0 <= a < 256. Static, filled with the other tables by the first call
-// on a device.
+// of 256 c f_t, fine[a][t] of a f_t, 0 <= a < 256. Static, each layer kind's filled by its first 8-bit append
+// or decode on a device (1.3 or 2.6 MB), which may be part of a capture.
 struct Kv8Angles {
   const float4* coarse;   // [kRopeCoarse][R]
   const float4* fine;     // [256][R]
 };
-cudaError_t upload_kv8_angles();                       // for the current device
-cudaError_t kv8_angles(bool global, Kv8Angles* out);   // after the upload
+cudaError_t kv8_angles(bool global, Kv8Angles* out);   // for the current device
 
 // a b - c d and its kind in two fp32 parts: products exact through fma, the sum's error kept, one rounding
 // at the end.

@@ -129,7 +129,6 @@ cudaError_t device_state(DeviceState* st) {
     G4_ADDR(g_rope_global_fine_t, s.global.fine_t);
 #undef G4_UPLOAD
 #undef G4_ADDR
-    if ((e = upload_kv8_angles()) != cudaSuccess) return e;
     const uint32_t zero = 0;
     if ((e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero))) != cudaSuccess) return e;
     if ((e = cudaGetSymbolAddress(&p, g_error_word)) != cudaSuccess) return e;

@@ -1,4 +1,8 @@
 """Promises of the header that the 8-bit cache's calls share with the bf16 ones, held to the bit."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -320,3 +324,71 @@ def test_a_cache_or_scratch_on_another_device_is_refused():
                               r.table, q)
     with pytest.raises(ValueError, match="the bf16 cache is on the CPU"):
         g4.g4attn_kv8_unpack(r.layer, i32([0]), i32([40]), r.cache.desc, r.table, scratch.desc, r.table)
+
+
+# ---- the first call ------------------------------------------------------------------------------------------
+
+FIRST_IN_A_CAPTURE = """
+import torch
+import invariant_hybrid_attention_gb300 as g4
+from invariant_hybrid_attention_gb300 import inputs as gi
+from invariant_hybrid_attention_gb300.paged import PagedKV8, device_int32
+for kind in ("sliding", "global"):
+    layer = g4.sliding_layer() if kind == "sliding" else g4.global_layer()
+    x = gi.bf16_normal((40, layer.n_kv_heads, layer.head_dim), 3).cuda()
+    v = x if kind == "sliding" else None
+    pos = device_int32(list(range(40)))
+    g4.g4attn_rope_apply(layer, x, pos, torch.empty_like(x))          # the library's first call: a bf16 one
+    rows = (device_int32([0]), device_int32([40]), device_int32([700]))
+    table = torch.arange(47, dtype=torch.int32, device="cuda")[None].contiguous()
+    one, two = PagedKV8(layer, 47), PagedKV8(layer, 47)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):                                      # the first 8-bit call of the process
+        g4.g4attn_kv8_append(layer, None, x, v, *rows, one.desc, table)
+    graph.replay()
+    torch.cuda.synchronize()
+    g4.g4attn_kv8_append(layer, None, x, v, *rows, two.desc, table)
+    torch.cuda.synchronize()
+    assert g4.g4attn_status_sync() == g4.G4_OK
+    assert torch.equal(one.pages, two.pages) and not (one.pages[-1] == 255).all()
+print("captured")
+"""
+
+
+FIRST_FROM_THREADS = """
+import threading
+import torch
+import invariant_hybrid_attention_gb300 as g4
+from invariant_hybrid_attention_gb300 import inputs as gi
+from invariant_hybrid_attention_gb300.paged import PagedKV8, device_int32
+layer = g4.global_layer()
+x, q = gi.bf16_normal((1, 4, 512), 3).cuda(), gi.bf16_normal((1, 32, 512), 4).cuda()
+table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+ws = [torch.empty(g4.g4attn_kv8_decode_workspace_bytes(layer, 1, 1), dtype=torch.uint8, device="cuda") for _ in range(8)]
+caches, outs = [PagedKV8(layer, 1) for _ in range(8)], [torch.empty_like(q) for _ in range(8)]
+streams, one = [torch.cuda.Stream() for _ in range(8)], device_int32([1])
+g4.load()
+torch.cuda.synchronize()
+start = threading.Barrier(8)
+def work(i):
+    start.wait()
+    g4.g4attn_kv8_decode(layer, None, q, x, None, one, caches[i].desc, table, outs[i], ws[i], stream=streams[i])
+threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+for t in threads: t.start()
+for t in threads: t.join()
+torch.cuda.synchronize()
+assert g4.g4attn_status_sync() == g4.G4_OK
+assert all(torch.equal(o, outs[0]) and torch.equal(c.pages[:, :, :1], caches[0].pages[:, :, :1]) for o, c in zip(outs, caches))
+assert outs[0].isfinite().all()
+print("threads")
+"""
+
+
+@pytest.mark.parametrize("script,word", [(FIRST_IN_A_CAPTURE, "captured"), (FIRST_FROM_THREADS, "threads")],
+                         ids=["captured", "threads"])
+def test_the_first_8_bit_calls_of_a_process(script, word):
+    """Captured, after a first bf16 call; and from eight threads at once. Each in a process of its own."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and word in p.stdout, p.stderr[-2000:]
