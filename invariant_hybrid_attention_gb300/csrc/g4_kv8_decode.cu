@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     }
   }
   const bool void_chunk = __syncthreads_or(bad);
-  const float qs[2] = {q_scale[2 * cq] * p.scale_log2, q_scale[2 * cq + 1] * p.scale_log2};
+  const float qs[2] = {q_scale[2 * cq], q_scale[2 * cq + 1]};
   const float q0[2] = {q_sum[0][2 * cq], q_sum[0][2 * cq + 1]}, q1[2] = {q_sum[1][2 * cq], q_sum[1][2 * cq + 1]};
 
   float o[S::kSegs * 8][4];   // O^T: rows = columns of V, columns = heads 2cq, 2cq + 1
@@ -422,14 +422,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv8_decode_kernel(const Decode
     const float ev_lo = v_lo == 255u ? NAN : (float)((int)v_lo - 133), ev_hi = v_hi == 255u ? NAN : (float)((int)v_hi - 133);
     const bool see_lo = key0 + gq >= k_begin && key0 + gq <= k_end;
     const bool see_hi = key0 + gq + 8 >= k_begin && key0 + gq + 8 <= k_end;
+    // the query's and the key's powers of two go together: either alone could leave fp32's range with large keys
     float x[4], y[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float sum0 = (s0[0][r] + s0[1][r]) + (s0[2][r] + s0[3][r]);
-      float s = fmaf(sum0, kUp, -q0[r & 1]) * kv8_step(r < 2 ? e_lo : e_hi);
-      if (GLOBAL) s += fmaf(s1[0][r] + s1[1][r], kUp, -q1[r & 1]) * kv8_step(r < 2 ? f_lo : f_hi);
+      float s = fmaf(sum0, kUp, -q0[r & 1]) * (qs[r & 1] * kv8_step(r < 2 ? e_lo : e_hi));
+      if (GLOBAL) s += fmaf(s1[0][r] + s1[1][r], kUp, -q1[r & 1]) * (qs[r & 1] * kv8_step(r < 2 ? f_lo : f_hi));
       const bool see = r < 2 ? see_lo : see_hi;
-      x[r] = see ? s * qs[r & 1] : -INFINITY;
+      x[r] = see ? s * p.scale_log2 : -INFINITY;
       y[r] = see ? x[r] + (r < 2 ? ev_lo : ev_hi) : -INFINITY;
     }
     float2 page_ms[2];

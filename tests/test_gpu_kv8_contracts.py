@@ -392,3 +392,18 @@ def test_the_first_8_bit_calls_of_a_process(script, word):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0 and word in p.stdout, p.stderr[-2000:]
+
+
+# ---- the largest keys -----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_decode_of_keys_near_the_largest_bf16(kind):
+    """Keys of size 2^113 under queries of size 2^-112: every product q.k, and every sum of them, is far inside
+    fp32's range, and so are the outputs."""
+    r = Rows(kind, [300, 40, 1100], seed=106, gap=0)
+    for x in r.k:
+        x.copy_((x.double() * 2.0 ** 113).bfloat16())
+    r.fill()
+    s = Step(r, weights=kind == "global", q_scale=2.0 ** -112)
+    s.run()
+    s.check()
