@@ -221,8 +221,9 @@ struct AppendArgs {
   int parts;   // warps per row
 };
 
-// Bound by the latency of its loads (24 warps an SM, the ALU pipe 55% busy): the 4 x 4096 sliding rows take
-// 79 us (402 MB, 5.1 TB/s), the 2 x 8192 global ones 27 us (109 MB, 4 TB/s).
+// The 4 x 4096 sliding rows take 79 us (402 MB, 5.1 TB/s, 1.33 times the copy's time), the 2 x 8192 global ones
+// 27 us (109 MB, 4 TB/s, 1.7 times). Neither memory nor issue (57%; the ALU pipe 55%) is full: 24 warps an SM
+// wait for their loads and for each other's results by turns.
 // One warp per (row, share of the KV heads). The row's angles are computed once for its heads, in two-part
 // arithmetic. Sliding: half a warp per vector, two heads at a time, K' and V together. Global: a warp
 // per head for S, then 8 lanes per head for the turned columns of up to four heads at once.

@@ -1,7 +1,8 @@
 // Decode over the 8-bit paged cache: one query token per request, its keys split into fixed chunks (512
 // keys on sliding layers, 1024 on global ones, aligned to key 0); inside a chunk page i goes to warp i % 4
 // and the warps' states merge in warp order, and the chunks' states merge by a tree fixed by the chunk
-// numbers. Every number a request gets depends on its own position, window and data. Where the page table
+// numbers. Every number a request gets depends on its own position, window and data, and every number of a
+// query head on that head alone (a rank's slice gives the full call's bits). Where the page table
 // holds one chunk at most (short contexts) the chunk's block writes the output itself, the bits that the
 // merge would give: a lone step of 37 keys takes 5.6 us instead of 7.5.
 //
