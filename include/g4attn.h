@@ -451,6 +451,71 @@ g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms
                             const g4attn_cache8* cache, const int32_t* page_table, int32_t max_pages,
                             float* page_weights, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The 4-bit paged cache ---------------------------------------------------------------------
+ * A cache of a quarter of the bytes: keys and values in microscaled 4-bit floating point. The RFC this library
+ * follows has no counterpart of it. The calls are those of the 8-bit cache, with the differences below.
+ *
+ * Values. A head vector x, normed and turned in fp32 (sliding: K' and V; global: S, and p-RoPE(K) on the 128 turned
+ * columns), is stored as E2M1 codes (a sign, and 0, 0.5, 1, 1.5, 2, 3, 4 or 6) with one power of two per block of 32
+ * consecutive columns (of the turned columns in the order [0, 64) then [256, 320)):
+ *   a = max |x| over the block,  E = floor(log2 a) - 2, and one more when a > 7 * 2^E (at most 125),
+ *   code = the step nearest to x / 2^E, ties to the even code, 6 at most; scale byte s = E + 127.
+ * No value is off by more than 2^E, a seventh to two sevenths of a. A block with a < 2^-77 is zeros with s = 0; when
+ * x holds an infinity or NaN, every block of the vector has s = 255 and zero codes and the vector reads as NaN. The
+ * value, code * 2^E, is a bf16 number. A key's bytes never depend on the batch, on the chunks its prompt came in, or
+ * on later tokens, so the calls below are batch-invariant like the bf16 ones.
+ *
+ * Layout. pages holds one block per (page, KV head), 16 keys each, blocks of
+ *   sliding 4368 bytes: [K' tile, 2048][V tile, 2048][scales of K', 16 x 8][of V, 16 x 8][tops of V, 16],
+ *   global 5456 bytes: [S tile, 4096][turned columns, 1024][scales of S, 16 x 16][of the turned, 16 x 4][tops of S, 16],
+ * at pages + (page * n_kv_heads + head) * block; a top is the largest scale byte of its key's vector. A wide tile is
+ * [columns / 256][16 keys][128 bytes]: a key's 16-byte piece c, at piece c ^ (j & 6) ^ 4 (j & 1), holds for each of
+ * the 8 blocks columns 4c .. 4c + 3, two codes a byte, the lower column in the low bits. The turned columns are
+ * [16 keys][64 bytes]: piece c holds for each of the 4 blocks columns 4c .. 4c + 3 and 16 + 4c .. 16 + 4c + 3.
+ * pages is 16-byte aligned. Slots that no key was written to may hold anything. */
+typedef struct {
+  void* pages;
+  int32_t num_pages;      /* physical pages */
+  int32_t page_size;      /* keys per page; must be 16 */
+} g4attn_cache4;
+
+/* Bytes of one page (all KV heads) of the layer's 4-bit cache; 0 for an unsupported layer. The RFC has
+ * no counterpart. */
+size_t g4attn_kv4_page_bytes(const g4attn_layer* layer);
+
+/* g4attn_kv8_append into a 4-bit cache (the RFC has no counterpart of it): arguments, row conventions, refusals
+ * and the limits on sequences that lost pages as there. */
+g4_status g4attn_kv4_append(const g4attn_layer* layer, const g4attn_norms* norms, const void* k, const void* v,
+                            int32_t T, const int32_t* q_start, const int32_t* q_len, const int32_t* ctx_start,
+                            int32_t B, const g4attn_cache4* cache, const int32_t* page_table, int32_t max_pages,
+                            void* stream);
+
+/* g4attn_kv8_unpack from a 4-bit cache (no counterpart in the RFC): reads keys back as bf16 pages. */
+g4_status g4attn_kv4_unpack(const g4attn_layer* layer, const int32_t* key_begin, const int32_t* key_end, int32_t B,
+                            const g4attn_cache4* cache, const int32_t* page_table, const g4attn_cache* out,
+                            const int32_t* out_table, int32_t max_pages, void* stream);
+
+/* g4attn_kv8_prefill over a 4-bit cache (no counterpart in the RFC): append, read-back of the visible keys into
+ * `scratch`, attention over them; every key and value, the new rows' own among them, is the stored 4-bit value. */
+g4_status g4attn_kv4_prefill(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k,
+                             const void* v, int32_t T, const int32_t* q_start, const int32_t* q_len,
+                             const int32_t* ctx_start, int32_t B, const int32_t* span, const g4attn_cache4* cache,
+                             const int32_t* page_table, const g4attn_cache* scratch, const int32_t* scratch_table,
+                             int32_t max_pages, void* out, void* stream);
+
+/* Bytes of workspace g4attn_kv4_decode needs (no counterpart in the RFC); page_weights: 1 when that
+ * call gets page_weights (global layers). 0 for an unsupported layer, B <= 0 or max_pages <= 0. */
+size_t g4attn_kv4_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, int32_t max_pages,
+                                         int32_t page_weights);
+
+/* g4attn_kv8_decode over a 4-bit cache (no counterpart in the RFC): arguments, fixed chunks, pos, page_weights,
+ * roundings and errors as there. A request with seq_len[b] = 0 (g4attn_plan_pages writes that for one it does not
+ * serve) holds no keys: nothing is appended for it, its row is zeros, and no error is set. */
+g4_status g4attn_kv4_decode(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k_new,
+                            const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B,
+                            const g4attn_cache4* cache, const int32_t* page_table, int32_t max_pages,
+                            float* page_weights, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Evicts whole pages from each sequence's page table by accumulated weight (no counterpart in the
  * RFC). Sequence b holds n = ceil(seq_len[b] / 16) pages. When n > keep_pages, the n - keep_pages lightest
  * of its evictable pages leave: all but the first first_pages and the last last_pages (first_pages >= 0,
@@ -467,6 +532,55 @@ g4_status g4attn_evict_pages(const int32_t* seq_len, const int32_t* page_table, 
                              int32_t max_pages, int32_t keep_pages, int32_t first_pages, int32_t last_pages,
                              int32_t* out_seq_len, int32_t* out_table, float* out_weights, int32_t* freed,
                              int32_t* n_freed, void* stream);
+
+/* ---- The page plan ------------------------------------------------------------------------------
+ * The pages of one layer kind: its free pages, its page table and what it keeps per request. All layers of a kind
+ * share one; a hybrid model has two (sliding and global). Every array is device memory, int32 unless said otherwise,
+ * and belongs to the caller. */
+typedef struct {
+  int32_t window;             /* 0: every key is kept; else the window of the sliding layers */
+  int32_t num_pages;          /* physical pages */
+  int32_t max_pages;          /* columns of page_table (and of freed) */
+  int32_t* free_pages;        /* [num_pages]: a ring of free physical pages */
+  const int32_t* pool;        /* [2]: where the free pages begin in the ring, and how many there are */
+  int32_t* out_pool;          /* [2]: the same after the step; may be pool */
+  int32_t* page_table;        /* [B][max_pages], read and written */
+  const int32_t* first_page;  /* [B], window > 0 only: the first logical page that a request still holds */
+  int32_t* out_first_page;    /* [B]: the same after the step; may be first_page */
+  const int32_t* lost;        /* [B] or NULL, window 0 only: keys that a request lost to evictions */
+  int32_t* out_lost;          /* [B]: the same after the step; may be lost */
+  const int32_t* freed;       /* [B][max_pages] and */
+  const int32_t* n_freed;     /* [B], or both NULL: the pages of the latest g4attn_evict_pages; with lost */
+  int32_t* seq_len;           /* [B] out: held keys, new ones included, of the served requests; 0 of the others */
+  int64_t* slots;             /* [T] out, or NULL: 16 * physical page + place in the page of each row's key; -1 for none */
+} g4attn_page_group;
+
+/* Plans one serving step on the device (the RFC has no counterpart): who is served, the page tables, and the rows'
+ * positions and slots, from the requests' lengths alone. Request b holds the keys of ctx_len[b] tokens (less lost[b]
+ * in a group that evicts) and wants new_len[b] more rows: a prompt or a chunk of one, 1 for a decode step, 0 for none;
+ * -1: it has ended. Groups: 1 or 2 (host array).
+ *   Rows are packed in the requests' order by new_len alone: q_start[b] is the sum of the new_len > 0 before b.
+ *   Served is a request with new_len[b] >= 1 whose rows end within T and which, in each group, needs no further page
+ *   or for which the pages that it and all requests before it need (served or not) are at most the free ones. Nothing
+ *   changes for a request that is not served: q_len[b] and seq_len[b] are 0, its rows' positions and slots -1.
+ *   A served request gets q_len[b] = new_len[b], out_ctx_len[b] = ctx_len[b] + new_len[b], its new pages in the table
+ *   (the j-th page that the step takes is the ring's j-th free one) and, in a group with a window, gives back the
+ *   pages wholly before its first new row's window. A request that has ended gives back all its pages, and its
+ *   ctx_len, first_page and lost become 0. The pages in freed come back too, and lost grows by 16 for each.
+ *   Pages come back behind the ring's end, in the requests' order (a request's evicted ones first), and can be taken
+ *   from the next step on. Table entries of pages given back are left as they are; no call reads them.
+ * ctx_start[b] = ctx_len[b]. positions, [T] or NULL: each row's RoPE position; -1 for rows of no request, those behind
+ * the last one among them. So q_start, q_len, ctx_start and a group's page_table are what a prefill takes; a decode
+ * step of new_len 1 for every request takes seq_len, page_table and (where keys were lost) positions as pos.
+ * out_ctx_len, q_len and ctx_start may be ctx_len or new_len's arrays, as long as no two outputs are one. A captured
+ * call can be replayed. 1 <= B <= 4096, T >= 0.
+ * Errors (G4_ERR_DEVICE): a length below -1, past 262144 or past a table, or state that contradicts it (lost, n_freed,
+ * first_page): the request is left as it is and not served. A pool whose place or count lies outside the ring: none
+ * of its pages are handed out or come back; more pages coming back than the ring has room for: none come back. A
+ * page outside [0, num_pages) in the ring, in freed or in a table: passed on (the row's slot is -1). */
+g4_status g4attn_plan_pages(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t T,
+                            const g4attn_page_group* groups, int32_t n_groups, int32_t* out_ctx_len, int32_t* q_start,
+                            int32_t* q_len, int32_t* ctx_start, int32_t* positions, void* stream);
 
 /* Runtime provenance (RFC section 4, rule 8): writes a NUL-terminated one-line record
  * (backend, kernel ids, schedule, split policy, accumulator, layer kind, device, dtype,

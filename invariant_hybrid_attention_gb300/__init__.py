@@ -29,7 +29,9 @@ EXPORTS = ("g4attn_rope_apply", "g4attn_prefill", "g4attn_prefill_stage", "g4att
            "g4attn_decode", "g4attn_decode_static", "g4attn_provenance", "g4attn_status_sync", "g4attn_status_string",
            "g4attn_set_wait_limit_ns", "g4attn_wait_limit_ns", "g4attn_prefill_partial", "g4attn_merge_partials",
            "g4attn_kv8_page_bytes", "g4attn_kv8_append", "g4attn_kv8_unpack", "g4attn_kv8_prefill",
-           "g4attn_kv8_decode_workspace_bytes", "g4attn_kv8_decode", "g4attn_evict_pages")
+           "g4attn_kv8_decode_workspace_bytes", "g4attn_kv8_decode", "g4attn_evict_pages",
+           "g4attn_kv4_page_bytes", "g4attn_kv4_append", "g4attn_kv4_unpack", "g4attn_kv4_prefill",
+           "g4attn_kv4_decode_workspace_bytes", "g4attn_kv4_decode", "g4attn_plan_pages")
 DEFAULT_WAIT_LIMIT_NS = 2_000_000_000   # the kernels' bounded waits give up after 2 s by default
 
 
@@ -57,6 +59,20 @@ class g4attn_cache8(ctypes.Structure):
     room = None      # its bytes and its device
 
 
+class g4attn_cache4(ctypes.Structure):
+    _fields_ = g4attn_cache8._fields_
+    tensor = None
+    room = None
+
+
+class g4attn_page_group(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)] + [
+        (name, ctypes.c_void_p) for name in ("free_pages", "pool", "out_pool", "page_table", "first_page", "out_first_page",
+                                             "lost", "out_lost", "freed", "n_freed", "seq_len", "slots")]
+    tensors = None   # make_page_group: what the fields point into
+    room = None      # its requests, rows (None: no slots) and device
+
+
 class G4Error(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} (status {status})")
@@ -78,6 +94,7 @@ def load(path: Optional[str] = None):
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     L, C = ctypes.POINTER(g4attn_layer), ctypes.POINTER(g4attn_cache)
     N, C8 = ctypes.POINTER(g4attn_norms), ctypes.POINTER(g4attn_cache8)
+    C4, G = ctypes.POINTER(g4attn_cache4), ctypes.POINTER(g4attn_page_group)
     sigs = {
         "g4attn_rope_apply": (I32, [L, P, P, I32, I32, P, P]),
         "g4attn_prefill": (I32, [L, P, P, P, I32, P, P, P, I32, C, P, I32, P, P]),
@@ -108,6 +125,13 @@ def load(path: Optional[str] = None):
         "g4attn_kv8_decode_workspace_bytes": (SZ, [L, I32, I32, I32]),
         "g4attn_kv8_decode": (I32, [L, N, P, P, P, P, P, I32, C8, P, I32, P, P, P, SZ, P]),
         "g4attn_evict_pages": (I32, [P, P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P]),
+        "g4attn_kv4_page_bytes": (SZ, [L]),
+        "g4attn_kv4_append": (I32, [L, N, P, P, I32, P, P, P, I32, C4, P, I32, P]),
+        "g4attn_kv4_unpack": (I32, [L, P, P, I32, C4, P, C, P, I32, P]),
+        "g4attn_kv4_prefill": (I32, [L, N, P, P, P, I32, P, P, P, I32, P, C4, P, C, P, I32, P, P]),
+        "g4attn_kv4_decode_workspace_bytes": (SZ, [L, I32, I32, I32]),
+        "g4attn_kv4_decode": (I32, [L, N, P, P, P, P, P, I32, C4, P, I32, P, P, P, SZ, P]),
+        "g4attn_plan_pages": (I32, [P, P, I32, I32, G, I32, P, P, P, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -360,17 +384,22 @@ def _torch_names():
     return _names
 
 
-def make_cache8(pages, num_pages: int) -> g4attn_cache8:
-    """pages: a dense tensor (or a raw address, which nothing checks) of num_pages pages."""
-    cache = g4attn_cache8(_ptr(pages), int(num_pages), PAGE_SIZE)
+def _make_quant(what: str, kind, pages, num_pages: int):
+    cache = kind(_ptr(pages), int(num_pages), PAGE_SIZE)
     if not isinstance(pages, int):
         if not pages.is_contiguous():
-            raise ValueError("make_cache8: pages must be dense")
+            raise ValueError(f"{what}: pages must be dense")
         cache.tensor, cache.room = pages, (pages.nbytes, pages.get_device())
     return cache
 
 
-_BLOCK8 = {256: 8224, 512: 10272}   # bytes of a page and KV head of an 8-bit cache, by head_dim
+def make_cache8(pages, num_pages: int) -> g4attn_cache8:
+    """pages: a dense tensor (or a raw address, which nothing checks) of num_pages pages."""
+    return _make_quant("make_cache8", g4attn_cache8, pages, num_pages)
+
+
+# bytes of a page and KV head of a quantised cache, by its kind and head_dim
+_BLOCK = {g4attn_cache8: {256: 8224, 512: 10272}, g4attn_cache4: {256: 4368, 512: 5456}}
 
 
 def _room16(what: str, cache: g4attn_cache):
@@ -402,9 +431,9 @@ def _pointers(what: str, stream, specs, layer=None, cache=None, bf16_cache=None)
         here = device()
     if cache is not None and cache.room is not None:
         room, at = cache.room
-        need = cache.num_pages * layer.n_kv_heads * _BLOCK8.get(layer.head_dim, 0)
+        need = cache.num_pages * layer.n_kv_heads * _BLOCK[cache.__class__].get(layer.head_dim, 0)
         if need > room or (at != here and here >= 0):
-            _refuse_pool(what, "the 8-bit cache", (room,), (need,), at, here)
+            _refuse_pool(what, f"the {8 if cache.__class__ is g4attn_cache8 else 4}-bit cache", (room,), (need,), at, here)
     if bf16_cache is not None:
         room, rot_room, at = bf16_cache.room or _room16(what, bf16_cache)
         blocks = bf16_cache.num_pages * layer.n_kv_heads
@@ -529,3 +558,134 @@ def g4attn_evict_pages(seq_len, page_table, page_weights, keep_pages: int, first
     _check((_lib or load()).g4attn_evict_pages(seq_len, page_table, page_weights, B, width, int(keep_pages),
                                                int(first_pages), int(last_pages), out_seq_len, out_table, out_weights,
                                                freed, n_freed, stream), "g4attn_evict_pages")
+
+
+# ---- the 4-bit paged cache ------------------------------------------------------------------------------
+
+def make_cache4(pages, num_pages: int) -> g4attn_cache4:
+    """pages: a dense tensor (or a raw address, which nothing checks) of num_pages pages."""
+    return _make_quant("make_cache4", g4attn_cache4, pages, num_pages)
+
+
+def g4attn_kv4_page_bytes(layer) -> int:
+    return int(load().g4attn_kv4_page_bytes(ctypes.byref(layer)))
+
+
+def g4attn_kv4_append(layer, norms, k, v, q_start, q_len, ctx_start, cache: g4attn_cache4, page_table, stream=None):
+    """g4attn_kv_append_normed into an 4-bit cache; norms may be None. Rows are turned by their held index: a
+    sequence that lost pages is continued by g4attn_kv4_decode with pos instead."""
+    bf, i32, _, _, _ = _names or _torch_names()
+    T, B, width = k.shape[0], q_start.shape[0], page_table.shape[-1]
+    kv, rows = (T, layer.n_kv_heads, layer.head_dim), (B,)
+    k, v, q_start, q_len, ctx_start, page_table, stream = _pointers("g4attn_kv4_append", stream, (
+        ("k", k, bf, kv), ("v", v, bf, kv), ("q_start", q_start, i32, rows), ("q_len", q_len, i32, rows),
+        ("ctx_start", ctx_start, i32, rows), ("page_table", page_table, i32, (B, width))),
+        layer, cache)
+    _check((_lib or load()).g4attn_kv4_append(ctypes.byref(layer), _opt(norms), k, v, T, q_start, q_len, ctx_start, B,
+                                              ctypes.byref(cache), page_table, width, stream), "g4attn_kv4_append")
+
+
+def g4attn_kv4_unpack(layer, key_begin, key_end, cache: g4attn_cache4, page_table, out: g4attn_cache, out_table,
+                      stream=None):
+    """Reads keys key_begin[b] .. key_end[b]-1 back as bf16 pages of `out` (through out_table)."""
+    _, i32, _, _, _ = _names or _torch_names()
+    B, width = key_begin.shape[0], page_table.shape[-1]
+    rows, table = (B,), (B, width)
+    key_begin, key_end, page_table, out_table, stream = _pointers("g4attn_kv4_unpack", stream, (
+        ("key_begin", key_begin, i32, rows), ("key_end", key_end, i32, rows), ("page_table", page_table, i32, table),
+        ("out_table", out_table, i32, table)), layer, cache, out)
+    _check((_lib or load()).g4attn_kv4_unpack(ctypes.byref(layer), key_begin, key_end, B, ctypes.byref(cache),
+                                              page_table, ctypes.byref(out), out_table, width, stream),
+           "g4attn_kv4_unpack")
+
+
+def g4attn_kv4_prefill(layer, norms, q, k, v, q_start, q_len, ctx_start, cache: g4attn_cache4, page_table,
+                       scratch: g4attn_cache, scratch_table, out, span=None, stream=None):
+    """A prefill (or chunk) over an 4-bit cache; scratch: a bf16 cache for the keys its rows see. Not for
+    sequences that lost pages (see g4attn_kv4_append)."""
+    bf, i32, _, _, _ = _names or _torch_names()
+    T, B, width = q.shape[0], q_start.shape[0], page_table.shape[-1]
+    qo, kv = (T, layer.n_q_heads, layer.head_dim), (T, layer.n_kv_heads, layer.head_dim)
+    rows, table = (B,), (B, width)
+    qp, k, v, q_start, q_len, ctx_start, span, page_table, scratch_table, op, stream = _pointers(
+        "g4attn_kv4_prefill", stream, (
+            ("q", q, bf, qo), ("k", k, bf, kv), ("v", v, bf, kv), ("q_start", q_start, i32, rows),
+            ("q_len", q_len, i32, rows), ("ctx_start", ctx_start, i32, rows), ("span", span, i32, (T, 2)),
+            ("page_table", page_table, i32, table), ("scratch_table", scratch_table, i32, table), ("out", out, bf, qo)),
+        layer, cache, scratch)
+    _check((_lib or load()).g4attn_kv4_prefill(ctypes.byref(layer), _opt(norms), qp, k, v, T, q_start, q_len, ctx_start,
+                                               B, span, ctypes.byref(cache), page_table, ctypes.byref(scratch),
+                                               scratch_table, width, op, stream), "g4attn_kv4_prefill")
+    return out
+
+
+def g4attn_kv4_decode_workspace_bytes(layer, B: int, max_pages: int, page_weights: bool = False) -> int:
+    return int(load().g4attn_kv4_decode_workspace_bytes(ctypes.byref(layer), int(B), int(max_pages),
+                                                        1 if page_weights else 0))
+
+
+def g4attn_kv4_decode(layer, norms, q, k_new, v_new, seq_len, cache: g4attn_cache4, page_table, out, workspace,
+                      pos=None, page_weights=None, stream=None):
+    """One decode step over an 4-bit cache. k_new None: the newest token is in the cache already; pos:
+    RoPE positions of sequences that lost pages; page_weights: accumulated per page (global layers)."""
+    bf, i32, f32, _, _ = _names or _torch_names()
+    B, width = q.shape[0], page_table.shape[-1]
+    qo, kv = (B, layer.n_q_heads, layer.head_dim), (B, layer.n_kv_heads, layer.head_dim)
+    rows, table = (B,), (B, width)
+    q, k_new, v_new, seq_len, pos, page_table, page_weights, op, work, stream = _pointers("g4attn_kv4_decode", stream, (
+        ("q", q, bf, qo), ("k_new", k_new, bf, kv), ("v_new", v_new, bf, kv), ("seq_len", seq_len, i32, rows),
+        ("pos", pos, i32, rows), ("page_table", page_table, i32, table), ("page_weights", page_weights, f32, table),
+        ("out", out, bf, qo), ("workspace", workspace, workspace.dtype, workspace.shape)),
+        layer, cache)
+    _check((_lib or load()).g4attn_kv4_decode(ctypes.byref(layer), _opt(norms), q, k_new, v_new, seq_len, pos, B,
+                                              ctypes.byref(cache), page_table, width, page_weights, op, work,
+                                              workspace.nbytes, stream), "g4attn_kv4_decode")
+    return out
+
+
+# ---- the page plan --------------------------------------------------------------------------------------
+
+def make_page_group(window: int, page_table, free_pages, pool, out_pool, seq_len, slots=None, first_page=None,
+                    out_first_page=None, lost=None, out_lost=None, freed=None, n_freed=None) -> g4attn_page_group:
+    """One layer kind's pages (window 0: a global one), as int32 tensors (slots: int64) on one device that the group
+    keeps. page_table [B, columns], free_pages [physical pages], pool [2]; slots [T]; the others [B] (freed as
+    page_table)."""
+    import torch
+    B, width = page_table.shape
+    tensors = dict(free_pages=free_pages, pool=pool, out_pool=out_pool, page_table=page_table, first_page=first_page,
+                   out_first_page=out_first_page, lost=lost, out_lost=out_lost, freed=freed, n_freed=n_freed,
+                   seq_len=seq_len, slots=slots)
+    shapes = dict(free_pages=(free_pages.numel(),), pool=(2,), out_pool=(2,), page_table=(B, width), freed=(B, width),
+                  slots=(None if slots is None else slots.numel(),))
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        dtype, shape = torch.int64 if name == "slots" else torch.int32, shapes.get(name, (B,))
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != page_table.device:
+            raise ValueError(f"make_page_group: {name} must be a dense {dtype} tensor of shape {shape} on "
+                             f"{page_table.device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                             f"{'' if t.is_contiguous() else ' (strided)'}")
+    group = g4attn_page_group(int(window), free_pages.numel(), width, *(_ptr(t) for t in tensors.values()))
+    group.tensors = tensors
+    group.room = (B, None if slots is None else slots.numel(), page_table.get_device())
+    return group
+
+
+def g4attn_plan_pages(ctx_len, new_len, groups, out_ctx_len, q_start, q_len, ctx_start, positions, stream=None):
+    """Plans one serving step of B requests and T = len(positions) rows over one or two page groups: who is served,
+    page tables, slots, positions. out_ctx_len may be ctx_len."""
+    _, i32, _, _, _ = _names or _torch_names()
+    B, T, n = ctx_len.shape[0], positions.shape[0], len(groups)
+    rows = (B,)
+    *pointers, stream = _pointers("g4attn_plan_pages", stream, (
+        ("ctx_len", ctx_len, i32, rows), ("new_len", new_len, i32, rows), ("out_ctx_len", out_ctx_len, i32, rows),
+        ("q_start", q_start, i32, rows), ("q_len", q_len, i32, rows), ("ctx_start", ctx_start, i32, rows),
+        ("positions", positions, i32, (T,))))
+    here = ctx_len.get_device()
+    for g in groups:
+        if g.room is not None and g.room != (B, T, here) and g.room != (B, None, here):
+            raise ValueError(f"g4attn_plan_pages: a group of {g.room[0]} requests, {g.room[1]} rows on device "
+                             f"{g.room[2]} in a call of {B} requests, {T} rows on device {here}")
+    array = groups if isinstance(groups, ctypes.Array) else (g4attn_page_group * n)(*groups)
+    _check((_lib or load()).g4attn_plan_pages(pointers[0], pointers[1], B, T, array, n, *pointers[2:], stream),
+           "g4attn_plan_pages")

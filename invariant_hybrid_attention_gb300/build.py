@@ -18,8 +18,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libg4attn.so")
 SOURCES = ["g4_api.cu", "g4_rope.cu", "g4_decode.cu", "g4_prefill.cu", "g4_prefill_global.cu",
-           "g4_kv8.cu", "g4_kv8_decode.cu"]
-HEADERS = ["g4_common.cuh", "g4_internal.h", "g4_prefill_common.cuh", "g4_kv8.cuh"]
+           "g4_kv8.cu", "g4_kv8_decode.cu", "g4_kv4.cu", "g4_kv4_decode.cu", "g4_plan.cu"]
+HEADERS = ["g4_common.cuh", "g4_internal.h", "g4_prefill_common.cuh", "g4_kv8.cuh", "g4_kv_rows.cuh",
+           "g4_kv_decode.cuh", "g4_kv4.cuh", "g4_plan.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]

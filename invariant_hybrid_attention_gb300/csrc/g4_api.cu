@@ -12,7 +12,9 @@
 #include <mutex>
 
 #include "g4_internal.h"
+#include "g4_kv4.cuh"
 #include "g4_kv8.cuh"
+#include "g4_plan.h"
 #include "g4attn.h"
 
 using namespace g4;
@@ -106,14 +108,30 @@ g4_status check_norms(const g4attn_norms* n, bool global, NormArgs* out) {
   return G4_OK;
 }
 
-g4_status check_cache8(const g4attn_cache8* c, const int32_t* page_table, int32_t max_pages) {
+// The quantised caches (8-bit and 4-bit) are called alike: their descriptors have the same fields, and the calls
+// the same arguments and checks. Quant: one cache kind's launches.
+struct Quant {
+  decltype(&launch_kv8_append) append;
+  decltype(&launch_kv8_append_decode) append_decode;
+  decltype(&launch_kv8_unpack) unpack;
+  decltype(&launch_kv8_decode) decode;
+  decltype(&kv8_decode_workspace_bytes) workspace_bytes;
+};
+constexpr Quant kQuant8{launch_kv8_append, launch_kv8_append_decode, launch_kv8_unpack, launch_kv8_decode,
+                        kv8_decode_workspace_bytes};
+constexpr Quant kQuant4{launch_kv4_append, launch_kv4_append_decode, launch_kv4_unpack, launch_kv4_decode,
+                        kv4_decode_workspace_bytes};
+
+template <class Cache>
+g4_status check_quant_cache(const Cache* c, const int32_t* page_table, int32_t max_pages) {
   if (!c || !c->pages || !aligned16(c->pages)) return G4_ERR_INVALID;
   if (c->page_size != kPage) return G4_ERR_UNSUPPORTED;
   if (c->num_pages <= 0 || max_pages <= 0 || !page_table) return G4_ERR_INVALID;
   return G4_OK;
 }
 
-PagedCache8 paged8(const g4attn_layer* L, const g4attn_cache8* c, const int32_t* page_table, int32_t max_pages) {
+template <class Cache>
+PagedCache8 paged_quant(const g4attn_layer* L, const Cache* c, const int32_t* page_table, int32_t max_pages) {
   return PagedCache8{(uint8_t*)c->pages, c->num_pages, page_table, max_pages, L->n_q_heads, L->n_kv_heads};
 }
 
@@ -139,6 +157,109 @@ cudaError_t decode_scratch(void** out) {
   }
   *out = g_scratch_ptr[dev];
   return cudaSuccess;
+}
+
+// ---- the calls over a quantised cache --------------------------------------------------------------------
+template <class Cache>
+g4_status quant_append(const Quant& quant, const g4attn_layer* layer, const g4attn_norms* norms, const void* k, const
+                       void* v, int32_t T, const int32_t* q_start, const int32_t* q_len, const int32_t* ctx_start,
+                       int32_t B, const Cache* cache, const int32_t* page_table, int32_t max_pages, void* stream) {
+  bool global = false;
+  g4_status s = check_layer(layer, &global);
+  if (s != G4_OK) return s;
+  NormArgs nm;
+  if ((s = check_norms(norms, global, &nm)) != G4_OK) return s;
+  if ((s = check_rows(k, T, q_start, q_len, ctx_start, B)) != G4_OK) return s;
+  if ((s = check_quant_cache(cache, page_table, max_pages)) != G4_OK) return s;
+  if (global ? v != nullptr : (T > 0 && (!v || !aligned16(v)))) return G4_ERR_INVALID;
+  if (T == 0) return G4_OK;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  const SeqRows rows{q_start, q_len, ctx_start, B, T};
+  return from_cuda(quant.append(global, k, v, rows, paged_quant(layer, cache, page_table, max_pages), nm, st,
+                   (cudaStream_t)stream));
+}
+
+template <class Cache>
+g4_status quant_unpack(const Quant& quant, const g4attn_layer* layer, const int32_t* key_begin, const int32_t* key_end,
+                       int32_t B, const Cache* cache, const int32_t* page_table, const g4attn_cache* out, const int32_t*
+                       out_table, int32_t max_pages, void* stream) {
+  bool global = false;
+  g4_status s = check_layer(layer, &global);
+  if (s != G4_OK) return s;
+  if (B <= 0 || !key_begin || !key_end) return G4_ERR_INVALID;
+  if ((s = check_quant_cache(cache, page_table, max_pages)) != G4_OK) return s;
+  if ((s = check_cache(out, global, out_table, max_pages)) != G4_OK) return s;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  const Kv8Range range{key_begin, key_end, SeqRows{nullptr, nullptr, nullptr, B, 0}, 0};
+  return from_cuda(quant.unpack(global, range, paged_quant(layer, cache, page_table, max_pages), paged(layer, out,
+                   out_table, max_pages), st, (cudaStream_t)stream));
+}
+
+template <class Cache>
+g4_status quant_prefill(const Quant& quant, const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const
+                        void* k, const void* v, int32_t T, const int32_t* q_start, const int32_t* q_len, const int32_t*
+                        ctx_start, int32_t B, const int32_t* span, const Cache* cache, const int32_t* page_table, const
+                        g4attn_cache* scratch, const int32_t* scratch_table, int32_t max_pages, void* out, void* stream)
+                        {
+  bool global = false;
+  g4_status s = check_layer(layer, &global);
+  if (s != G4_OK) return s;
+  NormArgs nm;
+  if ((s = check_norms(norms, global, &nm)) != G4_OK) return s;
+  if ((s = check_rows(q, T, q_start, q_len, ctx_start, B)) != G4_OK) return s;
+  if ((s = check_quant_cache(cache, page_table, max_pages)) != G4_OK) return s;
+  if ((s = check_cache(scratch, global, scratch_table, max_pages)) != G4_OK) return s;
+  if (T > 0 && (!k || !aligned16(k) || !out || !aligned16(out))) return G4_ERR_INVALID;
+  if (global ? v != nullptr : (T > 0 && (!v || !aligned16(v)))) return G4_ERR_INVALID;
+  if (span && (reinterpret_cast<uintptr_t>(span) & 7u)) return G4_ERR_INVALID;
+  if (T == 0) return G4_OK;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  const cudaStream_t cs = (cudaStream_t)stream;
+  const SeqRows rows{q_start, q_len, ctx_start, B, T, span};
+  const PagedCache8 pages = paged_quant(layer, cache, page_table, max_pages);
+  const PagedCache c16 = paged(layer, scratch, scratch_table, max_pages);
+  const int window = global ? 0 : layer->window;
+  if (quant.append(global, k, v, rows, pages, nm, st, cs) != cudaSuccess) return G4_ERR_CUDA;
+  const Kv8Range range{nullptr, nullptr, rows, window};
+  if (quant.unpack(global, range, pages, c16, st, cs) != cudaSuccess) return G4_ERR_CUDA;
+  // Plain queries are turned inside the attention kernel; normed ones, and those of a call with image
+  // spans, are staged in `out` first.
+  const bool staged = nm.any() || span != nullptr;
+  if (staged && launch_stage_queries(global, q, out, rows, c16, st, cs, nm) != cudaSuccess) return G4_ERR_CUDA;
+  return from_cuda(launch_prefill(global, rows, window, scale_log2(layer), c16, out, st, cs, staged ? nullptr : q));
+}
+
+template <class Cache>
+g4_status quant_decode(const Quant& quant, const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const
+                       void* k_new, const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B, const
+                       Cache* cache, const int32_t* page_table, int32_t max_pages, float* page_weights, void* out, void*
+                       workspace, size_t workspace_bytes, void* stream) {
+  bool global = false;
+  g4_status s = check_layer(layer, &global);
+  if (s != G4_OK) return s;
+  NormArgs nm;
+  if ((s = check_norms(norms, global, &nm)) != G4_OK) return s;
+  if (page_weights && !global) return G4_ERR_UNSUPPORTED;
+  if (B <= 0 || !q || !seq_len || !out || !workspace) return G4_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return G4_ERR_INVALID;
+  if (k_new ? !aligned16(k_new) || (global ? v_new != nullptr : (!v_new || !aligned16(v_new))) : v_new != nullptr)
+    return G4_ERR_INVALID;
+  if ((s = check_quant_cache(cache, page_table, max_pages)) != G4_OK) return s;
+  const int window = global ? 0 : layer->window;
+  if (workspace_bytes < quant.workspace_bytes(global, B, max_pages, window, layer->n_q_heads, layer->n_kv_heads,
+      page_weights != nullptr))
+    return G4_ERR_INVALID;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  const cudaStream_t cs = (cudaStream_t)stream;
+  const PagedCache8 pages = paged_quant(layer, cache, page_table, max_pages);
+  if (k_new && quant.append_decode(global, k_new, v_new, seq_len, pos, B, pages, nm, st, cs) != cudaSuccess)
+    return G4_ERR_CUDA;
+  return from_cuda(quant.decode(global, q, seq_len, pos, B, window, scale_log2(layer), pages, nm, page_weights, out,
+                   workspace, st, cs));
 }
 
 }  // namespace
@@ -453,36 +574,13 @@ g4_status g4attn_kv8_append(const g4attn_layer* layer, const g4attn_norms* norms
                             int32_t T, const int32_t* q_start, const int32_t* q_len, const int32_t* ctx_start,
                             int32_t B, const g4attn_cache8* cache, const int32_t* page_table, int32_t max_pages,
                             void* stream) {
-  bool global = false;
-  g4_status s = check_layer(layer, &global);
-  if (s != G4_OK) return s;
-  NormArgs nm;
-  if ((s = check_norms(norms, global, &nm)) != G4_OK) return s;
-  if ((s = check_rows(k, T, q_start, q_len, ctx_start, B)) != G4_OK) return s;
-  if ((s = check_cache8(cache, page_table, max_pages)) != G4_OK) return s;
-  if (global ? v != nullptr : (T > 0 && (!v || !aligned16(v)))) return G4_ERR_INVALID;
-  if (T == 0) return G4_OK;
-  DeviceState st;
-  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
-  const SeqRows rows{q_start, q_len, ctx_start, B, T};
-  return from_cuda(launch_kv8_append(global, k, v, rows, paged8(layer, cache, page_table, max_pages), nm, st,
-                                     (cudaStream_t)stream));
+  return quant_append(kQuant8, layer, norms, k, v, T, q_start, q_len, ctx_start, B, cache, page_table, max_pages, stream);
 }
 
 g4_status g4attn_kv8_unpack(const g4attn_layer* layer, const int32_t* key_begin, const int32_t* key_end, int32_t B,
                             const g4attn_cache8* cache, const int32_t* page_table, const g4attn_cache* out,
                             const int32_t* out_table, int32_t max_pages, void* stream) {
-  bool global = false;
-  g4_status s = check_layer(layer, &global);
-  if (s != G4_OK) return s;
-  if (B <= 0 || !key_begin || !key_end) return G4_ERR_INVALID;
-  if ((s = check_cache8(cache, page_table, max_pages)) != G4_OK) return s;
-  if ((s = check_cache(out, global, out_table, max_pages)) != G4_OK) return s;
-  DeviceState st;
-  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
-  const Kv8Range range{key_begin, key_end, SeqRows{nullptr, nullptr, nullptr, B, 0}, 0};
-  return from_cuda(launch_kv8_unpack(global, range, paged8(layer, cache, page_table, max_pages),
-                                     paged(layer, out, out_table, max_pages), st, (cudaStream_t)stream));
+  return quant_unpack(kQuant8, layer, key_begin, key_end, B, cache, page_table, out, out_table, max_pages, stream);
 }
 
 g4_status g4attn_kv8_prefill(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k,
@@ -490,33 +588,8 @@ g4_status g4attn_kv8_prefill(const g4attn_layer* layer, const g4attn_norms* norm
                              const int32_t* ctx_start, int32_t B, const int32_t* span, const g4attn_cache8* cache,
                              const int32_t* page_table, const g4attn_cache* scratch, const int32_t* scratch_table,
                              int32_t max_pages, void* out, void* stream) {
-  bool global = false;
-  g4_status s = check_layer(layer, &global);
-  if (s != G4_OK) return s;
-  NormArgs nm;
-  if ((s = check_norms(norms, global, &nm)) != G4_OK) return s;
-  if ((s = check_rows(q, T, q_start, q_len, ctx_start, B)) != G4_OK) return s;
-  if ((s = check_cache8(cache, page_table, max_pages)) != G4_OK) return s;
-  if ((s = check_cache(scratch, global, scratch_table, max_pages)) != G4_OK) return s;
-  if (T > 0 && (!k || !aligned16(k) || !out || !aligned16(out))) return G4_ERR_INVALID;
-  if (global ? v != nullptr : (T > 0 && (!v || !aligned16(v)))) return G4_ERR_INVALID;
-  if (span && (reinterpret_cast<uintptr_t>(span) & 7u)) return G4_ERR_INVALID;
-  if (T == 0) return G4_OK;
-  DeviceState st;
-  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
-  const cudaStream_t cs = (cudaStream_t)stream;
-  const SeqRows rows{q_start, q_len, ctx_start, B, T, span};
-  const PagedCache8 c8 = paged8(layer, cache, page_table, max_pages);
-  const PagedCache c16 = paged(layer, scratch, scratch_table, max_pages);
-  const int window = global ? 0 : layer->window;
-  if (launch_kv8_append(global, k, v, rows, c8, nm, st, cs) != cudaSuccess) return G4_ERR_CUDA;
-  const Kv8Range range{nullptr, nullptr, rows, window};
-  if (launch_kv8_unpack(global, range, c8, c16, st, cs) != cudaSuccess) return G4_ERR_CUDA;
-  // Plain queries are turned inside the attention kernel; normed ones, and those of a call with image
-  // spans, are staged in `out` first.
-  const bool staged = nm.any() || span != nullptr;
-  if (staged && launch_stage_queries(global, q, out, rows, c16, st, cs, nm) != cudaSuccess) return G4_ERR_CUDA;
-  return from_cuda(launch_prefill(global, rows, window, scale_log2(layer), c16, out, st, cs, staged ? nullptr : q));
+  return quant_prefill(kQuant8, layer, norms, q, k, v, T, q_start, q_len, ctx_start, B, span, cache, page_table,
+                       scratch, scratch_table, max_pages, out, stream);
 }
 
 size_t g4attn_kv8_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, int32_t max_pages,
@@ -531,29 +604,52 @@ g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms
                             const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B,
                             const g4attn_cache8* cache, const int32_t* page_table, int32_t max_pages,
                             float* page_weights, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return quant_decode(kQuant8, layer, norms, q, k_new, v_new, seq_len, pos, B, cache, page_table, max_pages,
+                      page_weights, out, workspace, workspace_bytes, stream);
+}
+
+size_t g4attn_kv4_page_bytes(const g4attn_layer* layer) {
   bool global = false;
-  g4_status s = check_layer(layer, &global);
-  if (s != G4_OK) return s;
-  NormArgs nm;
-  if ((s = check_norms(norms, global, &nm)) != G4_OK) return s;
-  if (page_weights && !global) return G4_ERR_UNSUPPORTED;
-  if (B <= 0 || !q || !seq_len || !out || !workspace) return G4_ERR_INVALID;
-  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return G4_ERR_INVALID;
-  if (k_new ? !aligned16(k_new) || (global ? v_new != nullptr : (!v_new || !aligned16(v_new))) : v_new != nullptr)
-    return G4_ERR_INVALID;
-  if ((s = check_cache8(cache, page_table, max_pages)) != G4_OK) return s;
-  const int window = global ? 0 : layer->window;
-  if (workspace_bytes < kv8_decode_workspace_bytes(global, B, max_pages, window, layer->n_q_heads, layer->n_kv_heads,
-                                                   page_weights != nullptr))
-    return G4_ERR_INVALID;
-  DeviceState st;
-  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
-  const cudaStream_t cs = (cudaStream_t)stream;
-  const PagedCache8 c8 = paged8(layer, cache, page_table, max_pages);
-  if (k_new && launch_kv8_append_decode(global, k_new, v_new, seq_len, pos, B, c8, nm, st, cs) != cudaSuccess)
-    return G4_ERR_CUDA;
-  return from_cuda(launch_kv8_decode(global, q, seq_len, pos, B, window, scale_log2(layer), c8, nm, page_weights, out,
-                                     workspace, st, cs));
+  if (check_layer(layer, &global) != G4_OK) return 0;
+  return (size_t)layer->n_kv_heads * (global ? Kv4Block<true>::kBytes : Kv4Block<false>::kBytes);
+}
+
+g4_status g4attn_kv4_append(const g4attn_layer* layer, const g4attn_norms* norms, const void* k, const void* v,
+                            int32_t T, const int32_t* q_start, const int32_t* q_len, const int32_t* ctx_start,
+                            int32_t B, const g4attn_cache4* cache, const int32_t* page_table, int32_t max_pages,
+                            void* stream) {
+  return quant_append(kQuant4, layer, norms, k, v, T, q_start, q_len, ctx_start, B, cache, page_table, max_pages, stream);
+}
+
+g4_status g4attn_kv4_unpack(const g4attn_layer* layer, const int32_t* key_begin, const int32_t* key_end, int32_t B,
+                            const g4attn_cache4* cache, const int32_t* page_table, const g4attn_cache* out,
+                            const int32_t* out_table, int32_t max_pages, void* stream) {
+  return quant_unpack(kQuant4, layer, key_begin, key_end, B, cache, page_table, out, out_table, max_pages, stream);
+}
+
+g4_status g4attn_kv4_prefill(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k,
+                             const void* v, int32_t T, const int32_t* q_start, const int32_t* q_len,
+                             const int32_t* ctx_start, int32_t B, const int32_t* span, const g4attn_cache4* cache,
+                             const int32_t* page_table, const g4attn_cache* scratch, const int32_t* scratch_table,
+                             int32_t max_pages, void* out, void* stream) {
+  return quant_prefill(kQuant4, layer, norms, q, k, v, T, q_start, q_len, ctx_start, B, span, cache, page_table,
+                       scratch, scratch_table, max_pages, out, stream);
+}
+
+size_t g4attn_kv4_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, int32_t max_pages,
+                                         int32_t page_weights) {
+  bool global = false;
+  if (check_layer(layer, &global) != G4_OK || B <= 0 || max_pages <= 0 || (page_weights && !global)) return 0;
+  return kv4_decode_workspace_bytes(global, B, max_pages, global ? 0 : layer->window, layer->n_q_heads,
+                                    layer->n_kv_heads, page_weights != 0);
+}
+
+g4_status g4attn_kv4_decode(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k_new,
+                            const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B,
+                            const g4attn_cache4* cache, const int32_t* page_table, int32_t max_pages,
+                            float* page_weights, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return quant_decode(kQuant4, layer, norms, q, k_new, v_new, seq_len, pos, B, cache, page_table, max_pages,
+                      page_weights, out, workspace, workspace_bytes, stream);
 }
 
 g4_status g4attn_evict_pages(const int32_t* seq_len, const int32_t* page_table, const float* page_weights, int32_t B,
@@ -570,6 +666,43 @@ g4_status g4attn_evict_pages(const int32_t* seq_len, const int32_t* page_table, 
   return from_cuda(launch_evict_pages(seq_len, page_table, page_weights, B, max_pages, keep_pages, first_pages,
                                       last_pages, out_seq_len, out_table, out_weights, freed, n_freed, st,
                                       (cudaStream_t)stream));
+}
+
+g4_status g4attn_plan_pages(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t T,
+                            const g4attn_page_group* groups, int32_t n_groups, int32_t* out_ctx_len, int32_t* q_start,
+                            int32_t* q_len, int32_t* ctx_start, int32_t* positions, void* stream) {
+  if (B <= 0 || B > kPlanRequests || T < 0) return G4_ERR_INVALID;
+  if (!groups || n_groups < 1 || n_groups > kPlanGroups) return G4_ERR_INVALID;
+  if (!ctx_len || !new_len || !out_ctx_len || !q_start || !q_len || !ctx_start) return G4_ERR_INVALID;
+  PlanArgs p{};
+  p.n_groups = n_groups;
+  p.B = B;
+  p.T = T;
+  for (int i = 0; i < n_groups; ++i) {
+    const g4attn_page_group& g = groups[i];
+    if (g.window < 0 || g.window > kMaxPos || g.num_pages <= 0 || g.max_pages <= 0) return G4_ERR_INVALID;
+    if (!g.free_pages || !g.pool || !g.out_pool || !g.page_table || !g.seq_len) return G4_ERR_INVALID;
+    if ((g.window > 0) != (g.first_page != nullptr) || (g.first_page != nullptr) != (g.out_first_page != nullptr))
+      return G4_ERR_INVALID;
+    if ((g.lost != nullptr) != (g.out_lost != nullptr) || (g.freed != nullptr) != (g.n_freed != nullptr))
+      return G4_ERR_INVALID;
+    if (g.window > 0 ? g.lost != nullptr || g.freed != nullptr : g.freed != nullptr && g.lost == nullptr)
+      return G4_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(g.slots) & 7u) return G4_ERR_INVALID;
+    p.group[i] = PlanGroup{g.window, g.num_pages, g.max_pages, g.free_pages, g.pool, g.out_pool, g.page_table,
+                           g.first_page, g.out_first_page, g.lost, g.out_lost, g.freed, g.n_freed, g.seq_len, g.slots};
+  }
+  p.ctx_len = ctx_len;
+  p.new_len = new_len;
+  p.out_ctx_len = out_ctx_len;
+  p.q_start = q_start;
+  p.q_len = q_len;
+  p.ctx_start = ctx_start;
+  p.positions = positions;
+  DeviceState st;
+  if (device_state(&st) != cudaSuccess) return G4_ERR_CUDA;
+  p.err = st.err;
+  return from_cuda(launch_plan_pages(p, (cudaStream_t)stream));
 }
 
 int32_t g4attn_provenance(const g4attn_layer* layer, char* buf, size_t len) {
@@ -590,6 +723,7 @@ int32_t g4attn_provenance(const g4attn_layer* layer, char* buf, size_t len) {
                  "qrope=attention-kernel(plain),append-pass(normed,vision,exact-decode);"
                  "exact-decode=prefill-kernels-one-row-chunks;vision=image-span-per-row;"
                  "kv8=int8-pow2-step-per-token-head,split-1024@abs-key0,weights:fp16-rne;"
+                 "kv4=e2m1-pow2-scale-per-32,split-1024@abs-key0,weights:fp16-rne;"
                  "accumulator=fp32;casts=roped-q,roped-k,p,out:bf16-rne;exp=ex2.approx.ftz.f32;device=%s;dtype=bf16;"
                  "shape=Hq%d,Hkv%d,D512,k_eq_v,prope0.25,theta1e6,scale%.9g;fallback=none",
                  dev, layer->n_q_heads, layer->n_kv_heads, (double)layer->softmax_scale);
@@ -602,6 +736,7 @@ int32_t g4attn_provenance(const g4attn_layer* layer, char* buf, size_t len) {
                  "qrope=attention-kernel(plain),append-pass(normed,vision,exact-decode);"
                  "exact-decode=prefill-kernels-one-row-chunks;vision=image-span-per-row;"
                  "kv8=int8-pow2-step-per-token-head,split-512@abs-key0,weights:fp16-rne;"
+                 "kv4=e2m1-pow2-scale-per-32,split-512@abs-key0,weights:fp16-rne;"
                  "accumulator=fp32;casts=roped-q,roped-k,p,out:bf16-rne;exp=ex2.approx.ftz.f32;device=%s;dtype=bf16;"
                  "shape=Hq%d,Hkv%d,D256,W%d,theta1e4,scale%.9g;fallback=none",
                  dev, layer->n_q_heads, layer->n_kv_heads, layer->window, (double)layer->softmax_scale);

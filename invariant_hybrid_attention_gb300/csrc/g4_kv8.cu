@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "g4_kv8.cuh"
+#include "g4_kv_rows.cuh"
 
 namespace g4 {
 
@@ -99,103 +100,6 @@ cudaError_t kv8_angles(bool global, Kv8Angles* out) {
 namespace {
 
 // ---- append: rows -> 8-bit pages ---------------------------------------------------------------------
-// D/16 lanes hold a head vector, 8 half-split pairs each (columns t0 .. t0+7 and D/2 + t0 .. +7), so
-// loads are 16 bytes a lane and the vector's largest |x| is one warp reduction.
-template <int D>
-struct Vec {
-  float a[8], b[8];   // columns t0 + i and D/2 + t0 + i
-};
-
-struct Raw {   // a lane's columns as bf16, as loaded
-  uint4 lo, hi;
-};
-
-template <int D>
-G4_DEV Raw load_raw(const __nv_bfloat16* __restrict__ src, int t0) {
-  return Raw{*reinterpret_cast<const uint4*>(src + t0), *reinterpret_cast<const uint4*>(src + D / 2 + t0)};
-}
-
-template <int D>
-G4_DEV Vec<D> widen(const Raw& raw) {
-  const uint4 lo = raw.lo, hi = raw.hi;
-  const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-  Vec<D> v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v.a[2 * i] = bf16_lo(lw[i]);
-    v.a[2 * i + 1] = bf16_hi(lw[i]);
-    v.b[2 * i] = bf16_lo(hw[i]);
-    v.b[2 * i + 1] = bf16_hi(hw[i]);
-  }
-  return v;
-}
-
-// sqrt(mean(x^2) + eps) over the D/16 lanes of the vector, and its reciprocal.
-struct Norm {
-  float root, inv;
-};
-
-template <int D>
-G4_DEV Norm norm_of(const Vec<D>& v, float eps) {
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(v.a[i], v.a[i], ss);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(v.b[i], v.b[i], ss);
-#pragma unroll
-  for (int o = 1; o < D / 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float root = __fsqrt_rn(__fadd_rn(ss * (1.0f / (float)D), eps));   // ss / D is exact: D is a power of 2
-  // an infinite root divides every number to 0: with root 0 the quotient below is x 0
-  return Norm{root == INFINITY ? 0.f : root, __frcp_rn(root)};
-}
-
-// x / root to the nearest, by Markstein's method: the product with the rounded reciprocal, corrected by its
-// exact remainder. What is rounded to a code next then agrees with the definition's division.
-G4_DEV float over(float x, Norm n) {
-  const float q = x * n.inv;
-  return fmaf(fmaf(-q, n.root, x), n.inv, q);
-}
-
-template <int D>
-G4_DEV void divide(Vec<D>& v, Norm n) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v.a[i] = over(v.a[i], n);
-    v.b[i] = over(v.b[i], n);
-  }
-}
-
-template <int D>
-G4_DEV void weight(Vec<D>& v, const __nv_bfloat16* __restrict__ w, int t0) {
-  const Vec<D> m = widen<D>(load_raw<D>(w, t0));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v.a[i] *= m.a[i];
-    v.b[i] *= m.b[i];
-  }
-}
-
-// max(a, |b|), NaN if either is one.
-G4_DEV float max_abs(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
-  return r;
-}
-
-// The bits of the largest |x| over the lanes of `mask` (all of which call it); a NaN wins.
-template <int D>
-G4_DEV uint32_t max_bits(const Vec<D>& v, unsigned mask) {
-  float m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    m[0] = max_abs(m[0], v.a[i]);
-    m[1] = max_abs(m[1], v.a[i + 1]);
-    m[2] = max_abs(m[2], v.b[i]);
-    m[3] = max_abs(m[3], v.b[i + 1]);
-  }
-  return __reduce_max_sync(mask, __float_as_uint(max_abs(max_abs(m[0], m[1]), max_abs(m[2], m[3]))));
-}
-
 // Stores the vector as key j of a tile (off_a, off_b: the offsets of columns t0 and of b[0] there); the lane
 // of column 0 stores the exponent.
 template <int D>
@@ -260,69 +164,12 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const AppendArgs p) 
     raw_v = load_raw<D>(v_row + (size_t)(g_lo + lane / LPV) * D, t0);
   }
 
-  int b = r, idx, pos;   // sequence, held index and RoPE position of the row's token
-  if (MODE == 0) {
-    int owner = -1;
-    for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
-      const int i = b0 + lane;
-      bool mine = false;
-      if (i < p.rows.B) {
-        const int qs = p.rows.q_start[i], L = p.rows.q_len[i];
-        if (L > 0) {
-          const bool ok = rows_ok(p.rows, qs, L, p.rows.ctx_start[i]);
-          if (!ok && unit == 0) set_error(p.err, kErrPos);
-          mine = ok && r >= qs && r - qs < L;
-        }
-      }
-      const unsigned m = __ballot_sync(0xffffffffu, mine);
-      if (m && owner < 0) owner = b0 + __ffs(m) - 1;
-      if (owner >= 0 && unit != 0) break;   // warp 0 looks at every sequence, for its error
-    }
-    if (owner < 0) return;
-    b = owner;
-    idx = p.rows.ctx_start[b] + (r - p.rows.q_start[b]);
-    pos = idx;
-  } else {
-    idx = p.seq_len[b] - 1;
-    pos = p.pos ? p.pos[b] : idx;
-  }
-  if (idx < 0 || idx >= kMaxPos || (idx >> 4) >= p.cache.max_pages || pos < idx || pos >= kMaxPos) {
-    if (lane == 0) set_error(p.err, kErrPos);
-    return;
-  }
-  const int phys = p.cache.page_table[(size_t)b * p.cache.max_pages + (idx >> 4)];
-  if (phys < 0 || phys >= p.cache.num_pages) {
-    if (lane == 0) set_error(p.err, kErrPage);
-    return;
-  }
+  int idx, pos, phys;
+  if (!token_place<MODE>(p.rows, p.seq_len, p.pos, p.cache, p.err, r, unit == 0, lane, idx, pos, phys)) return;
   const int j = idx & 15;
   uint8_t* page = p.cache.pages + (size_t)phys * HKV * Blk::kBytes;
-  // The row's angles: pair t by lane t % 32 (whole lines of the tables), then to the lanes that turn by
-  // them through shared memory, two pairs to 16 bytes, [i / 2][lane] so that the reads conflict on no bank.
   float2 cs[8];
-  {
-    const float4* cx = p.angles.coarse + (size_t)(pos >> 8) * R;
-    const float4* fx = p.angles.fine + (size_t)(pos & 255) * R;
-    float4 c4[R / 32], f4[R / 32];
-#pragma unroll
-    for (int k = 0; k < R / 32; ++k) {
-      c4[k] = __ldg(cx + 32 * k + lane);
-      f4[k] = __ldg(fx + 32 * k + lane);
-    }
-    float2* mine = angles[threadIdx.x >> 5];
-#pragma unroll
-    for (int k = 0; k < R / 32; ++k) {
-      const int t = 32 * k + lane;
-      mine[(((t & 7) >> 1) * (R / 8) + (t >> 3)) * 2 + (t & 1)] = rope_cs_exact(c4[k], f4[k]);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = *reinterpret_cast<const float4*>(mine + (i * (R / 8) + (tr >> 3)) * 2);
-      cs[2 * i] = make_float2(v.x, v.y);
-      cs[2 * i + 1] = make_float2(v.z, v.w);
-    }
-  }
+  row_angles<R>(p.angles, pos, lane, angles[threadIdx.x >> 5], tr, cs);
   const uint32_t off_a = kv8_offset(j, t0), off_b = kv8_offset(j, D / 2 + t0);
   if (GLOBAL) {
     Norm norm[4];   // of each head
@@ -375,42 +222,6 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const AppendArgs p) 
 }
 
 // ---- read-back: 8-bit pages -> bf16 pages --------------------------------------------------------------
-struct UnpackArgs {
-  Kv8Range range;
-  PagedCache8 src;
-  PagedCache dst;   // page_table: the destination pages of the same logical pages
-  uint32_t* err;
-};
-
-// The key range of sequence b; an impossible one is refused (empty, kErrPos).
-G4_DEV void key_range(const UnpackArgs& p, int b, int& lo, int& hi, uint32_t* err) {
-  lo = hi = 0;
-  if (p.range.key_begin) {
-    const int k0 = p.range.key_begin[b], k1 = p.range.key_end[b];
-    if (k1 <= k0) return;
-    if (k0 < 0 || k1 > kMaxPos || ((k1 - 1) >> 4) >= p.src.max_pages) {
-      set_error(err, kErrPos);
-      return;
-    }
-    lo = k0;
-    hi = k1;
-  } else {
-    const int L = p.range.rows.q_len[b], cs = p.range.rows.ctx_start[b];
-    if (L <= 0) return;
-    if (!rows_ok(p.range.rows, p.range.rows.q_start[b], L, cs) || ((cs + L - 1) >> 4) >= p.src.max_pages) {
-      set_error(err, kErrPos);
-      return;
-    }
-    lo = p.range.window > 0 ? max(0, cs - p.range.window + 1) : 0;
-    hi = cs + L;
-    // An image that began before this chunk holds its first row, whatever other rows it holds.
-    if (lo > 0 && p.range.rows.span) {
-      const int2 s = reinterpret_cast<const int2*>(p.range.rows.span)[p.range.rows.q_start[b]];
-      if (s.x >= 0 && s.x <= cs && cs < s.y && s.y <= hi) lo = min(lo, s.x);
-    }
-  }
-}
-
 // Sixteen stored bytes (one key's piece) as 16 bf16 values, in column order.
 G4_DEV void piece_bf16(const uint4& raw, float step, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -441,47 +252,16 @@ __global__ void __launch_bounds__(256) kv8_unpack_kernel(const UnpackArgs p) {
   const int lane = threadIdx.x & 31;
   const int HKV = p.src.hkv;
   const long long stride = (long long)gridDim.x * 8;
-  const int B = p.range.rows.B;
   // A prefill's attention multiplies the slots before a window's first key, in its page, by zero: they
   // are set to zero, since anything else might not be a number.
   const bool zero_before = p.range.key_begin == nullptr;
   long long base = 0;   // units before sequence group b0
   int b0 = 0;
   for (long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);; unit += stride) {
-    // find (sequence, logical page, head) of this unit, from where the last one was found
-    int b = -1, page = 0, g = 0;
-    while (b0 < B) {
-      int lo = 0, hi = 0;
-      if (b0 + lane < B) key_range(p, b0 + lane, lo, hi, p.err);
-      const int n = hi > lo ? (((hi - 1) >> 4) - (lo >> 4) + 1) : 0;
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
-      }
-      const long long first = base + (long long)(incl - n) * HKV, last = base + (long long)incl * HKV;
-      const unsigned m = __ballot_sync(0xffffffffu, unit >= first && unit < last);
-      if (m) {
-        const int s = __ffs(m) - 1;
-        const long long off = unit - __shfl_sync(0xffffffffu, first, s);
-        b = b0 + s;
-        page = (__shfl_sync(0xffffffffu, lo, s) >> 4) + (int)(off / HKV);
-        g = (int)(off % HKV);
-        break;
-      }
-      base += (long long)__shfl_sync(0xffffffffu, incl, 31) * HKV;
-      b0 += 32;
-    }
-    if (b < 0) return;
-    int lo, hi;
-    key_range(p, b, lo, hi, p.err);
-    const int from = p.src.page_table[(size_t)b * p.src.max_pages + page];
-    const int to = p.dst.page_table[(size_t)b * p.dst.max_pages + page];
-    if (from < 0 || from >= p.src.num_pages || to < 0 || to >= p.dst.num_pages) {
-      if (lane == 0) set_error(p.err, kErrPage);
-      continue;
-    }
+    int lo, hi, page, g, from, to;
+    const int found = find_page(p, unit, lane, base, b0, lo, hi, page, g, from, to);
+    if (found < 0) return;
+    if (found == 0) continue;
     const uint8_t* blk = p.src.pages + ((size_t)from * HKV + g) * Blk::kBytes;
     const size_t out = (size_t)to * HKV + g;
     __nv_bfloat16* k16 = (__nv_bfloat16*)p.dst.k + out * kPage * D;

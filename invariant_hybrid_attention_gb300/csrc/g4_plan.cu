@@ -1,0 +1,344 @@
+// The page plan of a serving step: which requests are served, their page tables, slots and positions, and the pages
+// that come back, in one launch.
+//
+// Every block goes through all requests (two scans over them: the rows and pages that each request wants, then the
+// pages that the served ones take and give back) and keeps the running sums in shared memory; then the blocks share
+// the rows, the taken pages and the returned pages out and find each one's request by bisection. So no sum travels
+// between blocks and nothing is kept in a workspace. The blocks are one cluster: its barrier stands between the last
+// read of the requests' state and the first write, so that the outputs may be the inputs.
+//
+// The free pages are a ring: pages are taken at its head and come back behind its tail, so that reads and writes of a
+// step never meet, and what comes back can be taken from the next step on. Every place is fixed by the requests'
+// order, not by timing.
+#include <atomic>
+
+#include "g4_kv8.cuh"
+#include "g4_plan.h"
+
+namespace g4 {
+
+namespace {
+
+constexpr int kThreads = 1024;
+
+G4_DEV int pages_of(int tokens) { return (tokens + kPage - 1) / kPage; }
+
+// Sums over the block before this thread, and of the whole block, of N values. buf: [2][N][32].
+template <int N>
+G4_DEV void block_scan(const uint32_t (&x)[N], uint32_t (&before)[N], uint32_t (&total)[N], uint32_t* buf) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t v = x[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += up;
+    }
+    before[i] = v - x[i];
+    if (lane == 31) buf[i * 32 + warp] = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t w = buf[i * 32 + lane];   // of warp `lane`
+    before[i] += __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
+    total[i] = __reduce_add_sync(0xffffffffu, w);
+  }
+  __syncthreads();
+}
+
+// The first i < n with end[i] > x (ends ascend; there is one).
+G4_DEV int owner_of(const uint32_t* end, int n, uint32_t x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (end[mid] > x)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+G4_DEV uint32_t start_of(const uint32_t* end, int i) { return i ? end[i - 1] : 0u; }
+
+G4_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+G4_DEV uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+
+// What the second half needs of a request, in shared memory, [field][request].
+enum Field { kRowEnd, kCtx, kTake0, kGive0, kLost0, kFirst0, kTake1, kGive1, kLost1, kFirst1, kFields };
+
+// K requests per thread.
+template <int K>
+__global__ void __launch_bounds__(kThreads) plan_pages_kernel(const PlanArgs p) {
+  extern __shared__ uint32_t req[];   // [kFields][B]
+  __shared__ uint32_t buf[4 * 32];
+  wait_for_grid();
+  let_next_grid_start();
+  const int B = p.B;
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  auto field = [&](int f) { return req + (size_t)f * B; };
+
+  // Each group's ring; one that contradicts itself gives and takes nothing.
+  uint32_t head[kPlanGroups], count[kPlanGroups];
+  bool sound[kPlanGroups];
+#pragma unroll
+  for (int g = 0; g < kPlanGroups; ++g) {
+    head[g] = count[g] = 0;
+    sound[g] = false;
+    if (g >= p.n_groups) continue;
+    const int h = p.group[g].pool[0], c = p.group[g].pool[1], n = p.group[g].num_pages;
+    sound[g] = h >= 0 && h < n && c >= 0 && c <= n;
+    if (!sound[g]) continue;
+    head[g] = (uint32_t)h;
+    count[g] = (uint32_t)c;
+  }
+
+  // ---- what each request wants: rows, and pages of each group
+  int ctx[K], add[K], held[K][kPlanGroups], first[K][kPlanGroups], lost[K][kPlanGroups], back[K][kPlanGroups];
+  bool ended[K], valid[K], served[K];
+  uint32_t need[K][kPlanGroups];
+  uint32_t sum[3] = {0, 0, 0};   // rows, pages
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int b = threadIdx.x * K + k;
+    const bool in = b < B;
+    ctx[k] = in ? p.ctx_len[b] : 0;
+    const int n = in ? p.new_len[b] : 0;
+    add[k] = n > 0 && n <= kMaxPos ? n : 0;   // its rows keep their place whether it is served or not
+    ended[k] = n == -1;
+    valid[k] = n >= -1 && n <= kMaxPos && ctx[k] >= 0 && ctx[k] <= kMaxPos - add[k];
+#pragma unroll
+    for (int g = 0; g < kPlanGroups; ++g) {
+      held[k][g] = first[k][g] = lost[k][g] = back[k][g] = 0;
+      if (g >= p.n_groups || !in) continue;
+      const PlanGroup& q = p.group[g];
+      if (q.first_page) first[k][g] = q.first_page[b];
+      if (q.lost) lost[k][g] = q.lost[b];
+      if (q.n_freed) back[k][g] = q.n_freed[b];
+      const int f = back[k][g], most = min(q.max_pages, kMaxPos / kPage);
+      valid[k] = valid[k] && f >= 0 && f <= most && lost[k][g] >= 0 && lost[k][g] <= ctx[k] - kPage * f;
+      held[k][g] = ctx[k] - (lost[k][g] + kPage * f);
+      valid[k] = valid[k] && pages_of(held[k][g] + add[k]) <= most && first[k][g] >= 0 && first[k][g] <= pages_of(held[k][g]);
+    }
+    sum[0] += (uint32_t)add[k];
+#pragma unroll
+    for (int g = 0; g < kPlanGroups; ++g) {
+      need[k][g] = valid[k] && g < p.n_groups ? (uint32_t)(pages_of(held[k][g] + add[k]) - pages_of(held[k][g])) : 0u;
+      sum[1 + g] += need[k][g];
+    }
+  }
+  uint32_t at[3], all[3];
+  block_scan<3>(sum, at, all, buf);
+  const uint32_t rows = all[0];
+
+  // ---- who is served, and what comes back
+  uint32_t move[4] = {0, 0, 0, 0};   // pages taken and given back, by group
+  uint32_t row_start[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int b = threadIdx.x * K + k;
+    row_start[k] = at[0];
+    at[0] += (uint32_t)add[k];
+    served[k] = valid[k] && add[k] > 0 && at[0] <= (uint32_t)p.T;
+#pragma unroll
+    for (int g = 0; g < kPlanGroups; ++g) {
+      at[1 + g] += need[k][g];
+      if (g < p.n_groups) served[k] = served[k] && (need[k][g] == 0 || at[1 + g] <= count[g]);
+    }
+    if (b < B) {
+      field(kRowEnd)[b] = at[0];
+      field(kCtx)[b] = (uint32_t)ctx[k] * 2u + (served[k] ? 1u : 0u);
+    }
+#pragma unroll
+    for (int g = 0; g < kPlanGroups; ++g) {
+      if (g >= p.n_groups) continue;
+      const int W = p.group[g].window;
+      if (!valid[k]) back[k][g] = 0;
+      const int now_lost = lost[k][g] + kPage * back[k][g];
+      int to = first[k][g];   // own pages first .. to - 1 go back, after the evicted ones
+      if (valid[k] && ended[k])
+        to = pages_of(held[k][g]);
+      else if (served[k] && W > 0)
+        to = max(to, max(0, held[k][g] - W + 1) / kPage);
+      if (b < B) {
+        field(kLost0 + 4 * g)[b] = (uint32_t)now_lost;
+        field(kFirst0 + 4 * g)[b] = (uint32_t)first[k][g] | ((uint32_t)back[k][g] << 16);   // both at most 16384
+      }
+      lost[k][g] = now_lost;
+      back[k][g] += to - first[k][g];
+      first[k][g] = to;
+      if (!served[k]) need[k][g] = 0;
+      move[2 * g] += need[k][g];
+      move[2 * g + 1] += (uint32_t)back[k][g];
+    }
+  }
+  uint32_t at4[4], all4[4];
+  block_scan<4>(move, at4, all4, buf);
+  bool give[kPlanGroups];
+#pragma unroll
+  for (int g = 0; g < kPlanGroups; ++g)
+    give[g] = g < p.n_groups && sound[g] && all4[2 * g + 1] <= (uint32_t)p.group[g].num_pages - count[g];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int b = threadIdx.x * K + k;
+    if (b >= B) continue;
+#pragma unroll
+    for (int g = 0; g < kPlanGroups; ++g) {
+      at4[2 * g] += need[k][g];
+      at4[2 * g + 1] += (uint32_t)back[k][g];
+      if (g >= p.n_groups) continue;
+      field(kTake0 + 4 * g)[b] = at4[2 * g];
+      field(kGive0 + 4 * g)[b] = at4[2 * g + 1];
+    }
+  }
+  __syncthreads();
+  cluster_sync();   // every block has read the state: from here on it is written
+
+  // ---- the requests' state, shared out by warps
+  if ((threadIdx.x >> 5) % ranks == rank) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int b = threadIdx.x * K + k;
+      if (b >= B) continue;
+      if (!valid[k]) set_error(p.err, kErrPos);
+      const int rows_of = served[k] ? add[k] : 0;
+      const bool gone = valid[k] && ended[k];
+      p.out_ctx_len[b] = gone ? 0 : ctx[k] + rows_of;
+      p.q_start[b] = (int32_t)row_start[k];
+      p.q_len[b] = rows_of;
+      p.ctx_start[b] = ctx[k];
+#pragma unroll
+      for (int g = 0; g < kPlanGroups; ++g) {
+        if (g >= p.n_groups) continue;
+        const PlanGroup& q = p.group[g];
+        q.seq_len[b] = served[k] ? held[k][g] + add[k] : 0;
+        if (q.out_first_page) q.out_first_page[b] = gone ? 0 : first[k][g];
+        if (q.out_lost) q.out_lost[b] = gone ? 0 : lost[k][g];
+      }
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < kPlanGroups; ++g) {
+    if (g >= p.n_groups || rank != 0 || threadIdx.x != 0) continue;
+    const PlanGroup& q = p.group[g];
+    if (!give[g]) set_error(p.err, kErrPage);
+    if (sound[g]) {
+      uint32_t h = head[g] + all4[2 * g];
+      if (h >= (uint32_t)q.num_pages) h -= (uint32_t)q.num_pages;
+      q.out_pool[0] = (int32_t)h;
+      q.out_pool[1] = (int32_t)(count[g] - all4[2 * g] + (give[g] ? all4[2 * g + 1] : 0u));
+    } else {
+      const int h = q.pool[0], c = q.pool[1];   // (only this thread writes out_pool)
+      q.out_pool[0] = h;
+      q.out_pool[1] = c;
+    }
+  }
+
+  // ---- rows: positions and slots
+  const uint32_t me = rank * kThreads + threadIdx.x, stride = ranks * kThreads;
+  for (uint32_t r = me; r < (uint32_t)p.T; r += stride) {
+    int pos = -1;
+    long long slot[kPlanGroups] = {-1, -1};
+    if (r < rows) {
+      const int b = owner_of(field(kRowEnd), B, r);
+      const uint32_t c = field(kCtx)[b];
+      if (c & 1u) {
+        const int ctx_b = (int)(c >> 1);
+        pos = ctx_b + (int)(r - start_of(field(kRowEnd), b));
+#pragma unroll
+        for (int g = 0; g < kPlanGroups; ++g) {
+          if (g >= p.n_groups) continue;
+          const PlanGroup& q = p.group[g];
+          const int lost_b = (int)field(kLost0 + 4 * g)[b], key = pos - lost_b, page = key >> 4;
+          const int past = page - pages_of(ctx_b - lost_b);   // >= 0: one of the pages taken now
+          int phys;
+          if (past >= 0) {
+            uint32_t i = head[g] + start_of(field(kTake0 + 4 * g), b) + (uint32_t)past;
+            if (i >= (uint32_t)q.num_pages) i -= (uint32_t)q.num_pages;
+            phys = q.free_pages[i];
+          } else {
+            phys = q.page_table[(size_t)b * q.max_pages + page];
+          }
+          slot[g] = phys < 0 || phys >= q.num_pages ? -1 : (long long)phys * kPage + (key & 15);
+          if (slot[g] < 0) set_error(p.err, kErrPage);
+        }
+      }
+    }
+    if (p.positions) p.positions[r] = pos;
+#pragma unroll
+    for (int g = 0; g < kPlanGroups; ++g)
+      if (g < p.n_groups && p.group[g].slots) p.group[g].slots[r] = slot[g];
+  }
+
+  // ---- pages taken and given back
+#pragma unroll
+  for (int g = 0; g < kPlanGroups; ++g) {
+    if (g >= p.n_groups) continue;
+    const PlanGroup& q = p.group[g];
+    const uint32_t n = (uint32_t)q.num_pages;
+    for (uint32_t i = me; i < all4[2 * g]; i += stride) {
+      const int b = owner_of(field(kTake0 + 4 * g), B, i);
+      const int held_b = (int)(field(kCtx)[b] >> 1) - (int)field(kLost0 + 4 * g)[b];
+      uint32_t from = head[g] + i;
+      if (from >= n) from -= n;
+      q.page_table[(size_t)b * q.max_pages + pages_of(held_b) + (i - start_of(field(kTake0 + 4 * g), b))] = q.free_pages[from];
+    }
+    if (!give[g]) continue;
+    for (uint32_t i = me; i < all4[2 * g + 1]; i += stride) {
+      const int b = owner_of(field(kGive0 + 4 * g), B, i);
+      const uint32_t off = i - start_of(field(kGive0 + 4 * g), b), f = field(kFirst0 + 4 * g)[b], evicted = f >> 16;
+      const int page = off < evicted ? q.freed[(size_t)b * q.max_pages + off]
+                                     : q.page_table[(size_t)b * q.max_pages + (f & 0xffffu) + (off - evicted)];
+      if (page < 0 || page >= q.num_pages) set_error(p.err, kErrPage);   // (a call that meets it later refuses it)
+      uint32_t to = head[g] + count[g] + i;
+      if (to >= n) to -= n;
+      q.free_pages[to] = page;
+    }
+  }
+}
+
+template <int K>
+cudaError_t launch(const PlanArgs& p, cudaStream_t s) {
+  static std::atomic<bool> done[64];   // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(plan_pages_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kFields * K * kThreads * (int)sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  // One block for small steps (a cluster takes longer to start), eight for others.
+  const unsigned blocks = p.T <= 2048 && p.B <= 512 ? 1 : 8;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = blocks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)kFields * p.B * sizeof(uint32_t);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, plan_pages_kernel<K>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_plan_pages(const PlanArgs& p, cudaStream_t s) {
+  return p.B <= kThreads ? launch<1>(p, s) : launch<kPlanRequests / kThreads>(p, s);
+}
+
+}  // namespace g4
