@@ -48,8 +48,8 @@ struct Shape {
   static_assert(kRing >= kWarps * kHeads * D * 4, "the warp merge reuses the ring");
 };
 
-constexpr uint32_t kDown = 40u << 23;            // factors are 2^(s - 127 - 40)
-constexpr float kUp = 1099511627776.0f;          // 2^40
+constexpr float kDown = 9.094947017729282e-13f;   // 2^-40: keeps every key's powers of two in fp32's range
+constexpr float kUp = 1099511627776.0f;           // 2^40
 
 G4_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
@@ -58,19 +58,20 @@ G4_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 2^(s - 167) of byte i of w: s >= 48 (a zero byte's sums are zeros, and finite times zero is zero).
-template <int I>
-G4_DEV float factor_of(uint32_t w) {
-  const uint32_t s = I == 3 ? (w >> 24) * (1u << 23) : (w & (0xffu << (8 * I))) * (1u << (23 - 8 * I));
-  return __uint_as_float(s - kDown);
+// d = a b.
+G4_DEV void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+      "%10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-G4_DEV float factor_at(const uint32_t* w, int b) {   // b known when compiled
-  switch (b & 3) {
-    case 0: return factor_of<0>(w[b >> 2]);
-    case 1: return factor_of<1>(w[b >> 2]);
-    case 2: return factor_of<2>(w[b >> 2]);
-  }
-  return factor_of<3>(w[b >> 2]);
+
+// The powers of two of the scale bytes of two neighbouring blocks, the low half of w. A zero byte gives (next to) 0, a
+// byte of 255 NaN.
+G4_DEV float2 two_powers(uint32_t w) {
+  uint32_t u;
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(u) : "h"((uint16_t)w));
+  return make_float2(bf16_lo(u), bf16_hi(u));
 }
 
 // Block of the q fragments that column d of a query head belongs to (see Shape::kQBlocks).
@@ -91,6 +92,11 @@ G4_DEV uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
+}
+// Stale scales above their key's top are cut to it (their weights are zeros); a NaN becomes 1.
+G4_DEV uint32_t at_most_one(uint32_t a) {
+  const __half2 h = __hmin2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(1.f));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 G4_DEV uint32_t mul_f16(uint32_t a, uint32_t b) {
   const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
@@ -289,31 +295,29 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<GLOBAL>::kResident) kv4_dec
     {
       constexpr int kQuarter = S::kBlocks / 4;
       const int pair = lane & 7, quarter = lane >> 3;
-      const uint32_t at = base + kVScale + 2 * pair * S::kBlocks + quarter * kQuarter;
-      uint32_t w0, w1;
-      if (GLOBAL) {
-        w0 = lds32(at);
-        w1 = lds32(at + S::kBlocks);
-      } else {
-        w0 = *reinterpret_cast<const uint16_t*>(blk + kVScale + 2 * pair * S::kBlocks + quarter * kQuarter);
-        w1 = *reinterpret_cast<const uint16_t*>(blk + kVScale + (2 * pair + 1) * S::kBlocks + quarter * kQuarter);
-      }
+      const uint8_t* at = blk + kVScale + 2 * pair * S::kBlocks + quarter * kQuarter;
       const uint32_t tops = *reinterpret_cast<const uint16_t*>(blk + Blk::kTop + 2 * pair);
-      const int t_0 = 127 - (int)(tops & 255u), t_1 = 127 - (int)(tops >> 8);
+      const float inv0 = __uint_as_float((uint32_t)max(254 - (int)(tops & 255u), 0) << 23);   // 2^(127 - top)
+      const float inv1 = __uint_as_float((uint32_t)max(254 - (int)(tops >> 8), 0) << 23);
 #pragma unroll
-      for (int i = 0; i < kQuarter; ++i) {
-        // (stale scales above the top are cut to it: their weights are zeros)
-        const int e0 = min(max((int)((w0 >> (8 * i)) & 255u) + t_0, 0), 127);
-        const int e1 = min(max((int)((w1 >> (8 * i)) & 255u) + t_1, 0), 127);
+      for (int i = 0; i < kQuarter; i += 2) {
+        const float2 f0 = two_powers(*reinterpret_cast<const uint16_t*>(at + i));
+        const float2 f1 = two_powers(*reinterpret_cast<const uint16_t*>(at + S::kBlocks + i));
         const int vb = quarter * kQuarter + i;
-        factors[((vb >> 1) * 4 + (pair & 3)) * 4 + (vb & 1) * 2 + (pair >> 2)] =
-            pack_f16(__uint_as_float((uint32_t)e0 << 23), __uint_as_float((uint32_t)e1 << 23));
+        uint32_t* to = factors + ((vb >> 1) * 4 + (pair & 3)) * 4 + (pair >> 2);
+        to[0] = at_most_one(pack_f16(f0.x * inv0, f1.x * inv1));
+        to[2] = at_most_one(pack_f16(f0.y * inv0, f1.y * inv1));
       }
     }
 
     // ---- S^T = K q^T: 16 keys x 8 heads, block by block
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    bool nan_lo, nan_hi;   // a NaN vector among the keys gq, gq + 8
+    auto add = [&](const float (&t)[4], float f_lo, float f_hi) {   // keys gq, gq + 8
+      s[0] = fmaf(t[0], f_lo, s[0]);
+      s[1] = fmaf(t[1], f_lo, s[1]);
+      s[2] = fmaf(t[2], f_hi, s[2]);
+      s[3] = fmaf(t[3], f_hi, s[3]);
+    };
     {
       uint32_t sc_lo[S::kBlocks / 4], sc_hi[S::kBlocks / 4];
       if (GLOBAL) {
@@ -323,8 +327,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<GLOBAL>::kResident) kv4_dec
         *reinterpret_cast<uint2*>(sc_lo) = lds64(base + Blk::kScale0 + gq * 8);
         *reinterpret_cast<uint2*>(sc_hi) = lds64(base + Blk::kScale0 + gq * 8 + 64);
       }
-      nan_lo = (sc_lo[0] & 255u) == 255u;
-      nan_hi = (sc_hi[0] & 255u) == 255u;
 #pragma unroll
       for (int sg = 0; sg < S::kSegs; ++sg) {
         const uint32_t at = base + sg * 2048 + k_lane;
@@ -338,18 +340,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<GLOBAL>::kResident) kv4_dec
           kv4_halves(y0w[w], a1);
           kv4_halves(x1w[w], c0);
           kv4_halves(y1w[w], c1);
+          const int vb = sg * 8 + 2 * w, qb = GLOBAL ? sg * 6 + 2 * w - 2 : vb;
+          const float2 f_lo = two_powers(sc_lo[vb / 4] >> (16 * (w & 1))), f_hi = two_powers(sc_hi[vb / 4] >> (16 * (w & 1)));
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const int vb = sg * 8 + 2 * w + u, qb = GLOBAL ? sg * 6 + 2 * w + u - 2 : vb;
-            const uint4 qf = lds128(q_addr + qb * 512);
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
-            mma(t, a0[2 * u], a1[2 * u], a0[2 * u + 1], a1[2 * u + 1], qf.x, qf.y);
+            const uint4 qf = lds128(q_addr + (qb + u) * 512);
+            float t[4];
+            mma_first(t, a0[2 * u], a1[2 * u], a0[2 * u + 1], a1[2 * u + 1], qf.x, qf.y);
             mma(t, c0[2 * u], c1[2 * u], c0[2 * u + 1], c1[2 * u + 1], qf.z, qf.w);
-            const float f_lo = factor_at(sc_lo, vb), f_hi = factor_at(sc_hi, vb);
-            s[0] = fmaf(t[0], f_lo, s[0]);
-            s[1] = fmaf(t[1], f_lo, s[1]);
-            s[2] = fmaf(t[2], f_hi, s[2]);
-            s[3] = fmaf(t[3], f_hi, s[3]);
+            add(t, (u ? f_lo.y : f_lo.x) * kDown, (u ? f_hi.y : f_hi.x) * kDown);
           }
         }
       }
@@ -358,39 +357,37 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<GLOBAL>::kResident) kv4_dec
         const uint4 x = lds128(at), y = lds128(at + 512);
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
         const uint32_t tc_lo = lds32(base + Blk::kScale1 + gq * 4), tc_hi = lds32(base + Blk::kScale1 + gq * 4 + 32);
-        nan_lo |= (tc_lo & 255u) == 255u;
-        nan_hi |= (tc_hi & 255u) == 255u;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t a0[4], a1[4];
           kv4_halves(xw[w], a0);
           kv4_halves(yw[w], a1);
+          const float2 f_lo = two_powers(tc_lo >> (8 * (w & 2))), f_hi = two_powers(tc_hi >> (8 * (w & 2)));
           const uint4 qf = lds128(q_addr + (12 + w) * 512);
-          float t[4] = {0.f, 0.f, 0.f, 0.f};
-          mma(t, a0[0], a1[0], a0[1], a1[1], qf.x, qf.y);
+          float t[4];
+          mma_first(t, a0[0], a1[0], a0[1], a1[1], qf.x, qf.y);
           mma(t, a0[2], a1[2], a0[3], a1[3], qf.z, qf.w);
-          const float f_lo = factor_at(&tc_lo, w), f_hi = factor_at(&tc_hi, w);
-          s[0] = fmaf(t[0], f_lo, s[0]);
-          s[1] = fmaf(t[1], f_lo, s[1]);
-          s[2] = fmaf(t[2], f_hi, s[2]);
-          s[3] = fmaf(t[3], f_hi, s[3]);
+          add(t, (w & 1 ? f_lo.y : f_lo.x) * kDown, (w & 1 ? f_hi.y : f_hi.x) * kDown);
         }
       }
     }
 
     // ---- softmax of this lane's keys gq, gq + 8 for heads 2cq, 2cq + 1
     const uint32_t v_lo = blk[Blk::kTop + gq], v_hi = blk[Blk::kTop + gq + 8];
-    const float ev_lo = v_lo == 255u ? NAN : (float)((int)v_lo - 127), ev_hi = v_hi == 255u ? NAN : (float)((int)v_hi - 127);
-    const bool see_lo = key0 + gq >= k_begin && key0 + gq <= k_end;
-    const bool see_hi = key0 + gq + 8 >= k_begin && key0 + gq + 8 <= k_end;
+    const float ev_lo = v_lo == 255u ? NAN : (float)((int)v_lo - 127);
+    const float ev_hi = v_hi == 255u ? NAN : (float)((int)v_hi - 127);
     float x[4], y[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const bool nan = r < 2 ? nan_lo : nan_hi;
-      const float score = nan ? NAN : (s[r] * qs[r & 1]) * kUp * p.scale_log2;
-      const bool see = r < 2 ? see_lo : see_hi;
-      x[r] = see ? score : -INFINITY;
-      y[r] = see ? x[r] + (r < 2 ? ev_lo : ev_hi) : -INFINITY;
+      x[r] = (s[r] * qs[r & 1]) * kUp * p.scale_log2;
+      y[r] = x[r] + (r < 2 ? ev_lo : ev_hi);
+    }
+    if (key0 < k_begin || key0 + kPage - 1 > k_end) {   // (the whole warp) keys outside are not seen
+      const bool see_lo = key0 + gq >= k_begin && key0 + gq <= k_end;
+      const bool see_hi = key0 + gq + 8 >= k_begin && key0 + gq + 8 <= k_end;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (!(r < 2 ? see_lo : see_hi)) x[r] = y[r] = -INFINITY;
     }
     float2 page_ms[2];
 #pragma unroll
