@@ -19,7 +19,6 @@ namespace g4 {
 
 namespace {
 
-constexpr int kThreads = 1024;
 
 G4_DEV int pages_of(int tokens) { return (tokens + kPage - 1) / kPage; }
 
@@ -41,7 +40,7 @@ G4_DEV void block_scan(const uint32_t (&x)[N], uint32_t (&before)[N], uint32_t (
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const uint32_t w = buf[i * 32 + lane];   // of warp `lane`
+    const uint32_t w = lane < (int)(blockDim.x >> 5) ? buf[i * 32 + lane] : 0u;   // of warp `lane`
     before[i] += __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
     total[i] = __reduce_add_sync(0xffffffffu, w);
   }
@@ -74,9 +73,9 @@ G4_DEV uint32_t cluster_size() {
 // What the second half needs of a request, in shared memory, [field][request].
 enum Field { kRowEnd, kCtx, kTake0, kGive0, kLost0, kFirst0, kTake1, kGive1, kLost1, kFirst1, kFields };
 
-// K requests per thread.
-template <int K>
-__global__ void __launch_bounds__(kThreads) plan_pages_kernel(const PlanArgs p) {
+// K requests per thread; a thread handles ITEMS neighbouring rows or pages together.
+template <int K, int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS) plan_pages_kernel(const PlanArgs p) {
   extern __shared__ uint32_t req[];   // [kFields][B]
   __shared__ uint32_t buf[4 * 32];
   wait_for_grid();
@@ -241,84 +240,144 @@ __global__ void __launch_bounds__(kThreads) plan_pages_kernel(const PlanArgs p) 
     }
   }
 
-  // ---- rows: positions and slots
-  const uint32_t me = rank * kThreads + threadIdx.x, stride = ranks * kThreads;
-  for (uint32_t r = me; r < (uint32_t)p.T; r += stride) {
-    int pos = -1;
-    long long slot[kPlanGroups] = {-1, -1};
-    if (r < rows) {
-      const int b = owner_of(field(kRowEnd), B, r);
-      const uint32_t c = field(kCtx)[b];
-      if (c & 1u) {
-        const int ctx_b = (int)(c >> 1);
-        pos = ctx_b + (int)(r - start_of(field(kRowEnd), b));
+  // ---- rows (positions and slots), pages taken, pages given back: a thread takes ITEMS neighbouring ones at a time,
+  // mostly of one request, so that it searches once and has their loads in flight together; the kinds of work follow one
+  // another in the threads' numbering, so that in a small step they run side by side.
+  auto do_rows = [&](uint32_t r0) {
+    int pos[ITEMS], page[ITEMS][kPlanGroups], place[ITEMS][kPlanGroups];
+    int b = -1;
+    uint32_t end = 0;
 #pragma unroll
-        for (int g = 0; g < kPlanGroups; ++g) {
-          if (g >= p.n_groups) continue;
-          const PlanGroup& q = p.group[g];
-          const int lost_b = (int)field(kLost0 + 4 * g)[b], key = pos - lost_b, page = key >> 4;
-          const int past = page - pages_of(ctx_b - lost_b);   // >= 0: one of the pages taken now
-          int phys;
-          if (past >= 0) {
-            uint32_t i = head[g] + start_of(field(kTake0 + 4 * g), b) + (uint32_t)past;
-            if (i >= (uint32_t)q.num_pages) i -= (uint32_t)q.num_pages;
-            phys = q.free_pages[i];
-          } else {
-            phys = q.page_table[(size_t)b * q.max_pages + page];
-          }
-          slot[g] = phys < 0 || phys >= q.num_pages ? -1 : (long long)phys * kPage + (key & 15);
-          if (slot[g] < 0) set_error(p.err, kErrPage);
-        }
+    for (int i = 0; i < ITEMS; ++i) {
+      const uint32_t r = r0 + i;
+      pos[i] = -1;
+#pragma unroll
+      for (int g = 0; g < kPlanGroups; ++g) page[i][g] = -1;
+      if (r >= rows || r >= (uint32_t)p.T) continue;
+      if (b < 0 || r >= end) {
+        b = owner_of(field(kRowEnd), B, r);
+        end = field(kRowEnd)[b];
+      }
+      const uint32_t c = field(kCtx)[b];
+      if (!(c & 1u)) continue;
+      const int ctx_b = (int)(c >> 1);
+      pos[i] = ctx_b + (int)(r - start_of(field(kRowEnd), b));
+#pragma unroll
+      for (int g = 0; g < kPlanGroups; ++g) {
+        if (g >= p.n_groups) continue;
+        const PlanGroup& q = p.group[g];
+        const int lost_b = (int)field(kLost0 + 4 * g)[b], key = pos[i] - lost_b;
+        const int past = (key >> 4) - pages_of(ctx_b - lost_b);   // >= 0: one of the pages taken now
+        uint32_t j = head[g] + start_of(field(kTake0 + 4 * g), b) + (uint32_t)past;
+        if (j >= (uint32_t)q.num_pages) j -= (uint32_t)q.num_pages;
+        page[i][g] = past >= 0 ? q.free_pages[j] : q.page_table[(size_t)b * q.max_pages + (key >> 4)];
+        place[i][g] = key & 15;
       }
     }
-    if (p.positions) p.positions[r] = pos;
 #pragma unroll
-    for (int g = 0; g < kPlanGroups; ++g)
-      if (g < p.n_groups && p.group[g].slots) p.group[g].slots[r] = slot[g];
-  }
-
-  // ---- pages taken and given back
+    for (int i = 0; i < ITEMS; ++i) {
+      const uint32_t r = r0 + i;
+      if (r >= (uint32_t)p.T) break;
+      if (p.positions) p.positions[r] = pos[i];
 #pragma unroll
-  for (int g = 0; g < kPlanGroups; ++g) {
-    if (g >= p.n_groups) continue;
-    const PlanGroup& q = p.group[g];
-    const uint32_t n = (uint32_t)q.num_pages;
-    for (uint32_t i = me; i < all4[2 * g]; i += stride) {
-      const int b = owner_of(field(kTake0 + 4 * g), B, i);
-      const int held_b = (int)(field(kCtx)[b] >> 1) - (int)field(kLost0 + 4 * g)[b];
-      uint32_t from = head[g] + i;
-      if (from >= n) from -= n;
-      q.page_table[(size_t)b * q.max_pages + pages_of(held_b) + (i - start_of(field(kTake0 + 4 * g), b))] = q.free_pages[from];
+      for (int g = 0; g < kPlanGroups; ++g) {
+        if (g >= p.n_groups) continue;
+        const bool in = page[i][g] >= 0 && page[i][g] < p.group[g].num_pages;
+        if (pos[i] >= 0 && !in) set_error(p.err, kErrPage);
+        if (p.group[g].slots) p.group[g].slots[r] = in ? (long long)page[i][g] * kPage + place[i][g] : -1;
+      }
     }
-    if (!give[g]) continue;
-    for (uint32_t i = me; i < all4[2 * g + 1]; i += stride) {
-      const int b = owner_of(field(kGive0 + 4 * g), B, i);
-      const uint32_t off = i - start_of(field(kGive0 + 4 * g), b), f = field(kFirst0 + 4 * g)[b], evicted = f >> 16;
-      const int page = off < evicted ? q.freed[(size_t)b * q.max_pages + off]
-                                     : q.page_table[(size_t)b * q.max_pages + (f & 0xffffu) + (off - evicted)];
-      if (page < 0 || page >= q.num_pages) set_error(p.err, kErrPage);   // (a call that meets it later refuses it)
-      uint32_t to = head[g] + count[g] + i;
-      if (to >= n) to -= n;
-      q.free_pages[to] = page;
+  };
+  auto do_takes = [&](int g, uint32_t i0, uint32_t total) {
+    const PlanGroup& q = p.group[g];
+    const uint32_t head_g = g ? head[1] : head[0];
+    const uint32_t* ends = field(kTake0 + 4 * g);
+    int page[ITEMS];
+    int32_t* to[ITEMS];
+    int b = -1;
+    uint32_t end = 0;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const uint32_t i = i0 + k;
+      to[k] = nullptr;
+      if (i >= total) continue;
+      if (b < 0 || i >= end) {
+        b = owner_of(ends, B, i);
+        end = ends[b];
+      }
+      const int held_b = (int)(field(kCtx)[b] >> 1) - (int)field(kLost0 + 4 * g)[b];
+      uint32_t from = head_g + i;
+      if (from >= (uint32_t)q.num_pages) from -= (uint32_t)q.num_pages;
+      page[k] = q.free_pages[from];
+      to[k] = q.page_table + (size_t)b * q.max_pages + pages_of(held_b) + (i - start_of(ends, b));
+    }
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      if (to[k]) *to[k] = page[k];
+  };
+  auto do_gives = [&](int g, uint32_t i0, uint32_t total) {
+    const PlanGroup& q = p.group[g];
+    const uint32_t tail = g ? head[1] + count[1] : head[0] + count[0];
+    const uint32_t* ends = field(kGive0 + 4 * g);
+    int page[ITEMS];
+    int b = -1;
+    uint32_t end = 0;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const uint32_t i = i0 + k;
+      page[k] = 0;
+      if (i >= total) continue;
+      if (b < 0 || i >= end) {
+        b = owner_of(ends, B, i);
+        end = ends[b];
+      }
+      const uint32_t off = i - start_of(ends, b), f = field(kFirst0 + 4 * g)[b], evicted = f >> 16;
+      page[k] = off < evicted ? q.freed[(size_t)b * q.max_pages + off]
+                              : q.page_table[(size_t)b * q.max_pages + (f & 0xffffu) + (off - evicted)];
+    }
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const uint32_t i = i0 + k;
+      if (i >= total) break;
+      if (page[k] < 0 || page[k] >= q.num_pages) set_error(p.err, kErrPage);   // (a call that meets it later refuses it)
+      uint32_t to = tail + i;
+      if (to >= (uint32_t)q.num_pages) to -= (uint32_t)q.num_pages;
+      q.free_pages[to] = page[k];
+    }
+  };
+  auto units = [](uint32_t n) { return (n + ITEMS - 1) / ITEMS; };
+  const uint32_t u_rows = units((uint32_t)p.T);
+  const uint32_t u_take0 = u_rows + units(all4[0]), u_give0 = u_take0 + (give[0] ? units(all4[1]) : 0u);
+  const uint32_t u_take1 = u_give0 + units(all4[2]), u_give1 = u_take1 + (give[1] ? units(all4[3]) : 0u);
+  for (uint32_t u = rank * THREADS + threadIdx.x; u < u_give1; u += ranks * THREADS) {
+    if (u < u_rows) {
+      do_rows(u * ITEMS);
+    } else {   // (one copy of the code for both groups: a small step runs it once, from memory)
+      const int g = u >= u_give0;
+      const uint32_t from = g ? u_give0 : u_rows, mid = g ? u_take1 : u_take0;
+      if (u < mid)
+        do_takes(g, (u - from) * ITEMS, g ? all4[2] : all4[0]);
+      else
+        do_gives(g, (u - mid) * ITEMS, g ? all4[3] : all4[1]);
     }
   }
 }
 
-template <int K>
-cudaError_t launch(const PlanArgs& p, cudaStream_t s) {
+template <int K, int THREADS, int ITEMS>
+cudaError_t launch(const PlanArgs& p, unsigned blocks, cudaStream_t s) {
   static std::atomic<bool> done[64];   // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(plan_pages_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kFields * K * kThreads * (int)sizeof(uint32_t));
+    e = cudaFuncSetAttribute(plan_pages_kernel<K, THREADS, ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kFields * K * THREADS * (int)sizeof(uint32_t));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(plan_pages_kernel<K, THREADS, ITEMS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
-  // One block for small steps (a cluster takes longer to start), eight for others.
-  const unsigned blocks = p.T <= 2048 && p.B <= 512 ? 1 : 8;
   cudaLaunchAttribute attr[2]{};
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -327,18 +386,23 @@ cudaError_t launch(const PlanArgs& p, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = (size_t)kFields * p.B * sizeof(uint32_t);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, plan_pages_kernel<K>, p);
+  cfg.numAttrs = blocks > 1 ? 2 : 1;   // (a lone block is a cluster of its own)
+  return cudaLaunchKernelEx(&cfg, plan_pages_kernel<K, THREADS, ITEMS>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_plan_pages(const PlanArgs& p, cudaStream_t s) {
-  return p.B <= kThreads ? launch<1>(p, s) : launch<kPlanRequests / kThreads>(p, s);
+  // Few requests: a small block, whose barriers are short, and one of them while its threads can take the rows in a few
+  // turns (64 decoding requests take 3.8 us, 300 mixed ones with 23 thousand rows 9.4 us, 12 with a cluster of 8). Many:
+  // two rows or pages a thread at a time (4096 requests, 105 thousand rows: 25.5 us; one 27.2, four 30.2).
+  if (p.B <= 256) return launch<1, 256, 1>(p, p.T <= 1024 ? 1 : 16, s);
+  if (p.B <= 1024) return launch<1, 1024, 1>(p, 16, s);
+  return launch<kPlanRequests / 1024, 1024, 2>(p, 16, s);
 }
 
 }  // namespace g4
