@@ -215,7 +215,7 @@ G4_DEV uint4 eight_bf16(uint32_t lo16, uint32_t hi16, float factor) {
 // >> 3) turns columns 8q .. 8q + 7 of every block of its key into core-matrix rows, so a warp store fills four whole
 // 128-byte core matrices.
 template <bool GLOBAL>
-__global__ void __launch_bounds__(256) kv4_unpack_kernel(const UnpackArgs p) {
+__global__ void __launch_bounds__(256, 4) kv4_unpack_kernel(const UnpackArgs p) {
   using Blk = Kv4Block<GLOBAL>;
   constexpr int D = Blk::D;
   wait_for_grid();
