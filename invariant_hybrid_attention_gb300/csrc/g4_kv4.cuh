@@ -49,7 +49,7 @@ __host__ __device__ constexpr int kv4_turned_piece(int j, int c) { return j * 64
 // into the exponent when the mantissa is above 1.75.
 G4_DEV uint32_t kv4_scale(uint32_t max_bits) {
   const uint32_t e = min((max_bits + 0x1fffffu) >> 23, 254u);
-  return e < 50u ? 0u : e - 2u;
+  return max_bits < (50u << 23) ? 0u : e - 2u;   // below 2^-77: zeros
 }
 
 // Eight consecutive columns as codes, column i in bits 4i .. 4i + 3 (scale: their block's byte, 0 and 255: zeros).

@@ -10,7 +10,8 @@ from typing import Optional
 
 import torch
 
-from . import PAGE_SIZE, g4attn_cache, g4attn_cache8, g4attn_kv8_page_bytes, make_cache, make_cache8
+from . import (PAGE_SIZE, g4attn_cache, g4attn_cache4, g4attn_cache8, g4attn_kv4_page_bytes, g4attn_kv8_page_bytes,
+               make_cache, make_cache4, make_cache8)
 
 
 ROT_DIMS = 128            # rotated columns of a global head: dims 0-63 and 256-319
@@ -118,6 +119,46 @@ def untile8(pages: torch.Tensor, head_dim: int):
         step = torch.where(e == 255, torch.full_like(e, 0x7FC00000), (e.clamp(8, 254) - 6) << 23).view(torch.float32)
         out.append((u.transpose(-4, -3).flatten(-3).float() - 128.0) * step[..., None])
         at += PAGE_SIZE * n
+    return out
+
+
+class PagedKV4:
+    """One layer's 4-bit paged cache: bytes [num_pages][n_kv_heads][block] (see include/g4attn.h)."""
+
+    def __init__(self, layer, num_pages: int, device="cuda", fill: Optional[int] = 255):
+        block = g4attn_kv4_page_bytes(layer) // int(layer.n_kv_heads)
+        self.pages = torch.empty((int(num_pages), int(layer.n_kv_heads), block), dtype=torch.uint8, device=device)
+        if fill is not None:
+            self.pages.fill_(fill)
+        self.num_pages = int(num_pages)
+
+    @property
+    def desc(self) -> g4attn_cache4:
+        return make_cache4(self.pages, self.num_pages)
+
+
+def untile4(pages: torch.Tensor, head_dim: int):
+    """The two tensors a 4-bit cache holds, as fp32 values [pages][heads][16][columns]: sliding K' and V,
+    global S and its 128 turned columns. Bytes [pages][heads][block] as in PagedKV4.pages."""
+    cols = (256, 256) if int(head_dim) == 256 else (512, ROT_DIMS)
+    j = torch.arange(PAGE_SIZE, device=pages.device)[:, None]
+    piece = torch.arange(8, device=pages.device)[None, :] ^ (j & 6) ^ ((j & 1) << 2)
+    steps = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, 0, -0.5, -1, -1.5, -2, -3, -4, -6], device=pages.device)
+    out, at, scale_at = [], 0, PAGE_SIZE * sum(cols) // 2
+    for n in cols:
+        u = pages[..., at:at + PAGE_SIZE * n // 2]
+        if n == ROT_DIMS:   # [key][piece][block][half][2 bytes] -> [key][block][half][piece][2 bytes]
+            u = u.unflatten(-1, (PAGE_SIZE, 4, 4, 2, 2)).movedim(-4, -2).flatten(-4)
+        else:               # [segment][key][piece][block][2 bytes] -> [key][segment][block][piece][2 bytes]
+            u = u.unflatten(-1, (n // 256, PAGE_SIZE, 8, 16))[..., j, piece, :].transpose(-4, -3)
+            u = u.unflatten(-1, (8, 2)).transpose(-3, -2).flatten(-4)
+        code = torch.stack([u & 15, u >> 4], -1).flatten(-2)                        # [pages][heads][16][n]
+        s = pages[..., scale_at:scale_at + PAGE_SIZE * n // 32].unflatten(-1, (PAGE_SIZE, n // 32))
+        factor = torch.where(s == 255, torch.full_like(s, float("nan"), dtype=torch.float32),
+                             torch.exp2(s.float() - 127.0))
+        out.append((steps[code.long()].unflatten(-1, (-1, 32)) * factor[..., None]).flatten(-2))
+        at += PAGE_SIZE * n // 2
+        scale_at += PAGE_SIZE * n // 32
     return out
 
 
