@@ -77,6 +77,20 @@ G4_DEV void store_line(const Line* line, uint8_t* tile, uint8_t* scales, uint8_t
   if (top && i == 7) top[j] = line->top;
 }
 
+// A sliding row's heads arrive through shared memory, two heads of K' and V (64 bytes a lane) to a stage, one stage ahead
+// of their use: a warp that held them in registers had its loads in flight for the codes' arithmetic alone, and waited
+// for them (4 x 4096 rows: 85 us, 70 so; two stages ahead, with fewer blocks an SM, 78).
+constexpr int kAhead = 1, kAppendStages = kAhead + 1, kAppendWarps = 4;
+
+G4_DEV void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+G4_DEV void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+G4_DEV void copies_wait() {   // until all but the latest N groups of this thread have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 struct AppendArgs {
   const __nv_bfloat16* k;
   const __nv_bfloat16* v;
@@ -95,15 +109,16 @@ struct AppendArgs {
 // arithmetic. Sliding: half a warp per vector, two heads at a time, K' then V. Global: a warp per head for S, then
 // 8 lanes per head for the turned columns of up to four heads at once.
 template <bool GLOBAL, bool NORM, int MODE>
-__global__ void __launch_bounds__(256, 3) kv4_append_kernel(const AppendArgs p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const AppendArgs p) {
   using Blk = Kv4Block<GLOBAL>;
   constexpr int D = Blk::D, R = Blk::R, LPV = D / 16;
-  __shared__ __align__(16) float2 angles[8][R];
-  __shared__ Line lines[8][4];
+  __shared__ __align__(16) float2 angles[kAppendWarps][R];
+  __shared__ Line lines[kAppendWarps][4];
+  __shared__ __align__(16) uint8_t staged[GLOBAL ? 16 : kAppendWarps * kAppendStages * 2048];   // [warp][stage][4][32 lanes][16]
   wait_for_grid();
   let_next_grid_start();
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long unit = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const int n_rows = MODE == 0 ? p.rows.T : p.rows.B;
   const long long r64 = unit / p.parts;
   if (r64 >= n_rows) return;
@@ -114,22 +129,37 @@ __global__ void __launch_bounds__(256, 3) kv4_append_kernel(const AppendArgs p) 
   const int tr = (lane % (R / 8)) * 8;   // and its turning ones (sliding: the same)
   const __nv_bfloat16* k_row = p.k + (size_t)r * HKV * D;
   const __nv_bfloat16* v_row = GLOBAL ? nullptr : p.v + (size_t)r * HKV * D;
-  // The row's loads are in flight while its sequence, page and angles are looked up: all of a global
-  // row's (four heads at most, and the turned columns again, 8 lanes a head), the first two heads' of a
-  // sliding one, whose others follow two heads ahead.
-  Raw raw[4], raw_turned, raw_v;
+  // The row's loads are in flight while its sequence, page and angles are looked up: all of a global row's (four heads
+  // at most, and the turned columns again, 8 lanes a head), the first stages of a sliding one.
+  Raw raw[4], raw_turned;
+  uint8_t* stage = staged + (threadIdx.x >> 5) * kAppendStages * 2048 + lane * 16;   // a lane reads what it copied
+  auto fetch = [&](int n) {   // sliding: heads g_lo + 2n + {0, 1}, half a warp each
+    const int g = g_lo + 2 * n + lane / LPV;
+    if (g < g_hi) {
+      const uint32_t to = smem_u32(stage + n % kAppendStages * 2048);
+      const __nv_bfloat16 *k = k_row + (size_t)g * D + t0, *v = v_row + (size_t)g * D + t0;
+      copy16(to, k);
+      copy16(to + 512, k + D / 2);
+      copy16(to + 1024, v);
+      copy16(to + 1536, v + D / 2);
+    }
+    copies_commit();
+  };
   if (GLOBAL) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i < per) raw[i] = load_raw<D>(k_row + (size_t)(g_lo + i) * D, t0);
     if ((lane >> 3) < per) raw_turned = load_raw<D>(k_row + (size_t)(g_lo + (lane >> 3)) * D, tr);
   } else {
-    raw[0] = load_raw<D>(k_row + (size_t)(g_lo + lane / LPV) * D, t0);
-    raw_v = load_raw<D>(v_row + (size_t)(g_lo + lane / LPV) * D, t0);
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) fetch(n);
   }
 
   int idx, pos, phys;
-  if (!token_place<MODE>(p.rows, p.seq_len, p.pos, p.cache, p.err, r, unit == 0, lane, idx, pos, phys, true)) return;
+  if (!token_place<MODE>(p.rows, p.seq_len, p.pos, p.cache, p.err, r, unit == 0, lane, idx, pos, phys, true)) {
+    if (!GLOBAL) copies_wait<0>();
+    return;
+  }
   const int j = idx & 15;
   uint8_t* page = p.cache.pages + (size_t)phys * HKV * Blk::kBytes;
   float2 cs[8];
@@ -173,14 +203,13 @@ __global__ void __launch_bounds__(256, 3) kv4_append_kernel(const AppendArgs p) 
     const unsigned mask = 0xffffu << (lane & 16);
     Line* mine = line + 2 * (lane >> 4);
 #pragma unroll 1
-    for (int g0 = g_lo; g0 < g_hi; g0 += 2) {
-      const int g = g0 + lane / LPV;
+    for (int n = 0; 2 * n < per; ++n) {
+      const int g = g_lo + 2 * n + lane / LPV;
       uint8_t* blk = page + (size_t)g * Blk::kBytes;
-      Vec<D> k = widen<D>(raw[0]), v = widen<D>(raw_v);
-      if (g0 + 2 < g_hi) {
-        raw[0] = load_raw<D>(k_row + (size_t)(g + 2) * D, t0);
-        raw_v = load_raw<D>(v_row + (size_t)(g + 2) * D, t0);
-      }
+      copies_wait<kAhead - 1>();
+      const uint4* got = reinterpret_cast<const uint4*>(stage + n % kAppendStages * 2048);
+      Vec<D> k = widen<D>(Raw{got[0], got[32]}), v = widen<D>(Raw{got[64], got[96]});
+      fetch(n + kAhead);   // (into the stage that was read a turn ago)
       if (NORM && p.nm.wk) {
         divide<D>(k, norm_of<D>(k, p.nm.eps));
         weight<D>(k, p.nm.wk, t0);
@@ -292,11 +321,11 @@ cudaError_t append(AppendArgs& a, int n_rows, cudaStream_t s) {
   const int most = a.cache.hkv / (GLOBAL ? 1 : 2);
   a.parts = 1;
   while (a.parts < most && (long long)n_rows * a.parts < 152 * 32) a.parts *= 2;
-  const long long blocks = ((long long)n_rows * a.parts + 7) / 8;
+  const long long blocks = ((long long)n_rows * a.parts + kAppendWarps - 1) / kAppendWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (a.nm.any())
-    return launch_early(kv4_append_kernel<GLOBAL, true, MODE>, (unsigned)blocks, 256, 0, s, a);
-  return launch_early(kv4_append_kernel<GLOBAL, false, MODE>, (unsigned)blocks, 256, 0, s, a);
+    return launch_early(kv4_append_kernel<GLOBAL, true, MODE>, (unsigned)blocks, kAppendWarps * 32, 0, s, a);
+  return launch_early(kv4_append_kernel<GLOBAL, false, MODE>, (unsigned)blocks, kAppendWarps * 32, 0, s, a);
 }
 
 }  // namespace
