@@ -472,7 +472,7 @@ g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms
  * [columns / 256][16 keys][128 bytes]: a key's 16-byte piece c, at piece c ^ (j & 6) ^ 4 (j & 1), holds for each of
  * the 8 blocks columns 4c .. 4c + 3, two codes a byte, the lower column in the low bits. The turned columns are
  * [16 keys][64 bytes]: piece c holds for each of the 4 blocks columns 4c .. 4c + 3 and 16 + 4c .. 16 + 4c + 3.
- * pages is 16-byte aligned. Slots that no key was written to may hold anything. */
+ * pages is 16-byte aligned. Scale bytes are 0, 48 .. 252 or 255. Slots that no key was written to may hold anything. */
 typedef struct {
   void* pages;
   int32_t num_pages;      /* physical pages */
@@ -510,7 +510,9 @@ size_t g4attn_kv4_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, i
 
 /* g4attn_kv8_decode over a 4-bit cache (no counterpart in the RFC): arguments, fixed chunks, pos, page_weights,
  * roundings and errors as there. A request with seq_len[b] = 0 (g4attn_plan_pages writes that for one it does not
- * serve) holds no keys: nothing is appended for it, its row is zeros, and no error is set. */
+ * serve) holds no keys: nothing is appended for it, its row is zeros, and no error is set. The value product takes a
+ * block's scale relative to the largest of its key's vector, in fp16: a block more than 2^24 below that one counts as
+ * zeros there (not in the scores, and not in g4attn_kv4_prefill). */
 g4_status g4attn_kv4_decode(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k_new,
                             const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B,
                             const g4attn_cache4* cache, const int32_t* page_table, int32_t max_pages,
@@ -572,8 +574,9 @@ typedef struct {
  * ctx_start[b] = ctx_len[b]. positions, [T] or NULL: each row's RoPE position; -1 for rows of no request, those behind
  * the last one among them. So q_start, q_len, ctx_start and a group's page_table are what a prefill takes; a decode
  * step of new_len 1 for every request takes seq_len, page_table and (where keys were lost) positions as pos.
- * out_ctx_len, q_len and ctx_start may be ctx_len or new_len's arrays, as long as no two outputs are one. A captured
- * call can be replayed. 1 <= B <= 4096, T >= 0.
+ * out_ctx_len, q_len and ctx_start may be ctx_len or new_len's arrays, as long as no two outputs are one; two groups
+ * share no array. A captured call can be replayed. The plan knows no image spans: the pages of an image that began
+ * before its chunk's window are not kept for it. 1 <= B <= 4096, T >= 0.
  * Errors (G4_ERR_DEVICE): a length below -1, past 262144 or past a table, or state that contradicts it (lost, n_freed,
  * first_page): the request is left as it is and not served. A pool whose place or count lies outside the ring: none
  * of its pages are handed out or come back; more pages coming back than the ring has room for: none come back. A

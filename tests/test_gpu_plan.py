@@ -231,6 +231,40 @@ def test_slots_past_32_bits():
     assert pool.tolist() == [6, 0]
 
 
+def test_outputs_over_the_inputs_and_groups_without_slots():
+    p = Plan([20, 40, 0, 70], [1, 30, 5, -1], 40, windows=(0, 32), spare=9, seed=6)
+    want = p.device()
+    p.call(want)
+    d = p.device(in_place=True)
+    for x in d["groups"]:
+        t = x["group"].tensors
+        x["group"] = g4.make_page_group(x["group"].window, t["page_table"], t["free_pages"], t["pool"], t["out_pool"],
+                                        t["seq_len"], None, **{k: t[k] for k in ("first_page", "out_first_page", "lost",
+                                                                                 "out_lost", "freed", "n_freed")})
+    g4.g4attn_plan_pages(d["ctx"], d["new"], [x["group"] for x in d["groups"]], d["ctx"], d["q_start"], d["new"],
+                         d["ctx_start"], d["pos"])
+    status_ok()
+    assert torch.equal(d["ctx"], want["out_ctx"]) and torch.equal(d["new"], want["q_len"])
+    assert torch.equal(d["pos"], want["pos"]) and torch.equal(d["ctx_start"], want["ctx_start"])
+    for x, y in zip(d["groups"], want["groups"]):
+        assert torch.equal(x["table"], y["table"]) and torch.equal(x["ring"], y["ring"])
+        assert torch.equal(x["pool"], y["out_pool"]) and (x["slots"] == -99).all()
+
+
+def test_two_plans_at_once():
+    """Of two batches, on two streams, with states of their own."""
+    plans = [Plan([20 + i, 400, 0, 70] * 80, [1, 30, 5, -1] * 80, 4000, spare=500, seed=i) for i in (1, 2)]
+    states, streams = [p.device() for p in plans], [torch.cuda.Stream() for _ in plans]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, d, stream in zip(plans, states, streams):
+            with torch.cuda.stream(stream):
+                p.call(d)
+    status_ok()
+    for p, d in zip(plans, states):
+        p.check(d)
+
+
 def test_groups_of_other_sizes_are_refused():
     p = Plan([20, 40], [1, 1], 4)
     d, other = p.device(), Plan([20, 40, 1], [1, 1, 1], 4).device()
