@@ -16,6 +16,21 @@
 //            own maximum grows by more than 2^8, so w_j <= 2^15.
 // Declared roundings: roped q to bf16, w to fp16 (2^-11 relative, each weight by itself), the output to bf16; all sums
 // are fp32.
+//
+// What bounds it. Not the page stream: 64 requests of 1k to 32k keys take 365 us on a global layer (1.23 GB, 3.4 TB/s,
+// 50% of the measured copy rate) and 81 us on a sliding one (0.29 GB, 3.6 TB/s), where the 8-bit cache's decode takes
+// 391 and 90 for twice the bytes. A page-head block of 5456 bytes costs its warp about 1000 instructions: 256 are
+// conversions of code pairs (every global S value is needed twice, in pairs of columns for the scores and in pairs of keys
+// for the values), 64 order the keys' pairs, 64 are matrix instructions. The ALU pipe, which takes one instruction in two
+// cycles and gives way to the matrix pipe, is 52% busy, and two warps a scheduler (128 output registers a thread) cover
+// the rest of the chain's latency only in part (2.0 instructions a cycle). A lone request of 37 keys takes 5.3 us, of
+// 16384 keys 29, of 131072 keys 72 (512 blocks on 304 places).
+// Built, measured and not kept (us for the mix; kept: 374 timed alone with cold caches): two warps a page, one per
+// 256 columns, with 12 warps an SM: 426; the same with two pages a step and the softmax shared out: 373 to 396; the
+// scores of page n + 1 and the values of page n in one stretch of code: 424; two pages a warp together: 414 (the loop
+// then outgrows the instruction caches). Shifts as multiplications on the other pipe: 375 to 383. Chunks of 512 keys: 436,
+// and 25 instead of 30 for a lone request of 16384. On sliding layers chunks of 256, 1024 and 2048 keys take 98, 82 and
+// 81 against 85, and a lone request of 4096 keys 15, 22 and 23 against 17.
 #include <atomic>
 
 #include "g4_kv4.cuh"

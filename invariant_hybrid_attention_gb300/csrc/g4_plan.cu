@@ -10,6 +10,10 @@
 // The free pages are a ring: pages are taken at its head and come back behind its tail, so that reads and writes of a
 // step never meet, and what comes back can be taken from the next step on. Every place is fixed by the requests'
 // order, not by timing.
+//
+// Bound by latency: a chain of loads, two scans, a search, a load and a store, and in a small step by the instructions
+// themselves, which come from memory (a version with its loops unrolled over four items took 10.3 us instead of 3.9 for
+// 64 decoding requests).
 #include <atomic>
 
 #include "g4_kv8.cuh"
