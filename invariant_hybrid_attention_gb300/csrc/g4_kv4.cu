@@ -108,8 +108,8 @@ struct AppendArgs {
 // One warp per (row, share of the KV heads). The row's angles are computed once for its heads, in two-part
 // arithmetic. Sliding: half a warp per vector, two heads at a time, K' then V. Global: a warp per head for S, then
 // 8 lanes per head for the turned columns of up to four heads at once.
-// The 4 x 4096 sliding rows take 70 us (340 MB, 4.8 TB/s, 73% of the copy rate; the ALU pipe 55%, 2.9 instructions a
-// cycle), the 2 x 8192 global ones 29 us (111 MB; a warp's row is one round of loads and then its arithmetic).
+// The 4 x 4096 sliding rows take 70 us (340 MB, 4.8 TB/s, 72% of the copy rate; the ALU pipe 55%, 2.9 instructions a
+// cycle), the 2 x 8192 global ones 37 us timed by events, some 6 of which an empty stretch reads too (89 MB).
 template <bool GLOBAL, bool NORM, int MODE>
 __global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const AppendArgs p) {
   using Blk = Kv4Block<GLOBAL>;
@@ -242,7 +242,7 @@ G4_DEV uint4 eight_bf16(uint32_t lo16, uint32_t hi16, float factor) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Bound by memory: the 4 x 4096 sliding rows take 54 us (340 MB, 6.3 TB/s).
+// Bound by its loads: the 4 x 4096 sliding rows take 54 us (56 with cold caches; 340 MB, 6.1 to 6.3 TB/s).
 // One warp per (page, KV head), walking the batch's pages in a grid-sized stride. Lane (key kk = lane & 7, q = lane
 // >> 3) turns columns 8q .. 8q + 7 of every block of its key into core-matrix rows, so a warp store fills four whole
 // 128-byte core matrices.

@@ -26,7 +26,7 @@
 // the rest of the chain's latency only in part (2.0 instructions a cycle). A lone request of 37 keys takes 5.3 us, of
 // 16384 keys 29, of 131072 keys 72 (512 blocks on 304 places).
 // Built, measured and not kept (us for the mix; kept: 374 timed alone with cold caches): two warps a page, one per
-// 256 columns, with 12 warps an SM: 426; the same with two pages a step and the softmax shared out: 373 to 396; the
+// 256 columns, with 12 warps an SM: 425; the same with two pages a step and the softmax shared out: 373 to 396; the
 // scores of page n + 1 and the values of page n in one stretch of code: 424; two pages a warp together: 414 (the loop
 // then outgrows the instruction caches). Shifts as multiplications on the other pipe: 375 to 383. Chunks of 512 keys: 436,
 // and 25 instead of 30 for a lone request of 16384. On sliding layers chunks of 256, 1024 and 2048 keys take 98, 82 and
