@@ -601,7 +601,7 @@ def g4attn_kv4_unpack(layer, key_begin, key_end, cache: g4attn_cache4, page_tabl
 
 def g4attn_kv4_prefill(layer, norms, q, k, v, q_start, q_len, ctx_start, cache: g4attn_cache4, page_table,
                        scratch: g4attn_cache, scratch_table, out, span=None, stream=None):
-    """A prefill (or chunk) over an 4-bit cache; scratch: a bf16 cache for the keys its rows see. Not for
+    """A prefill (or chunk) over a 4-bit cache; scratch: a bf16 cache for the keys its rows see. Not for
     sequences that lost pages (see g4attn_kv4_append)."""
     bf, i32, _, _, _ = _names or _torch_names()
     T, B, width = q.shape[0], q_start.shape[0], page_table.shape[-1]
@@ -626,7 +626,7 @@ def g4attn_kv4_decode_workspace_bytes(layer, B: int, max_pages: int, page_weight
 
 def g4attn_kv4_decode(layer, norms, q, k_new, v_new, seq_len, cache: g4attn_cache4, page_table, out, workspace,
                       pos=None, page_weights=None, stream=None):
-    """One decode step over an 4-bit cache. k_new None: the newest token is in the cache already; pos:
+    """One decode step over a 4-bit cache. k_new None: the newest token is in the cache already; pos:
     RoPE positions of sequences that lost pages; page_weights: accumulated per page (global layers)."""
     bf, i32, f32, _, _ = _names or _torch_names()
     B, width = q.shape[0], page_table.shape[-1]

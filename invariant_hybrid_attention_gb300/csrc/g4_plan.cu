@@ -13,7 +13,9 @@
 //
 // Bound by latency: a chain of loads, two scans, a search, a load and a store, and in a small step by the instructions
 // themselves, which come from memory (a version with its loops unrolled over four items took 10.3 us instead of 3.9 for
-// 64 decoding requests).
+// 64 decoding requests). Of 4096 requests' 24 us some 7 are the loads and what is computed of them, 3 the scans, 1 the
+// state, 7 the 110 thousand rows and 6 the pages, by leaving parts out; a row costs the same without its loads or its stores, and searching
+// on from the last owner in place of a bisection gains nothing.
 #include <atomic>
 
 #include "g4_kv8.cuh"
@@ -22,7 +24,6 @@
 namespace g4 {
 
 namespace {
-
 
 G4_DEV int pages_of(int tokens) { return (tokens + kPage - 1) / kPage; }
 
@@ -74,19 +75,38 @@ G4_DEV uint32_t cluster_size() {
   return r;
 }
 
+// Thread t's K neighbouring values of n.
+template <int K>
+G4_DEV void get(const int32_t* from, int t, int n, int (&x)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) x[k] = t * K + k < n ? from[t * K + k] : 0;
+}
+// To shared memory (16-byte aligned, with room for the last thread's K); four of them in one store, which has no bank
+// conflicts (4096 requests: 25.5 -> 24.2 us).
+template <int K>
+G4_DEV void put(uint32_t* to, int t, const uint32_t (&x)[K]) {
+  if (K == 4)
+    reinterpret_cast<uint4*>(to)[t] = make_uint4(x[0], x[1 % K], x[2 % K], x[3 % K]);
+  else
+#pragma unroll
+    for (int k = 0; k < K; ++k) to[t * K + k] = x[k];
+}
+
 // What the second half needs of a request, in shared memory, [field][request].
 enum Field { kRowEnd, kCtx, kTake0, kGive0, kLost0, kFirst0, kTake1, kGive1, kLost1, kFirst1, kFields };
 
 // K requests per thread; a thread handles ITEMS neighbouring rows or pages together.
 template <int K, int THREADS, int ITEMS>
 __global__ void __launch_bounds__(THREADS) plan_pages_kernel(const PlanArgs p) {
-  extern __shared__ uint32_t req[];   // [kFields][B]
+  extern __shared__ __align__(16) uint32_t req[];   // [kFields][B up to K]
   __shared__ uint32_t buf[4 * 32];
   wait_for_grid();
   let_next_grid_start();
   const int B = p.B;
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
-  auto field = [&](int f) { return req + (size_t)f * B; };
+  const int pad = (B + K - 1) / K * K;
+  auto field = [&](int f) { return req + (size_t)f * pad; };
+  const bool any = threadIdx.x * K < B;
 
   // Each group's ring; one that contradicts itself gives and takes nothing.
   uint32_t head[kPlanGroups], count[kPlanGroups];
@@ -108,23 +128,36 @@ __global__ void __launch_bounds__(THREADS) plan_pages_kernel(const PlanArgs p) {
   bool ended[K], valid[K], served[K];
   uint32_t need[K][kPlanGroups];
   uint32_t sum[3] = {0, 0, 0};   // rows, pages
+  get<K>(p.ctx_len, threadIdx.x, B, ctx);
+  get<K>(p.new_len, threadIdx.x, B, add);
+#pragma unroll
+  for (int g = 0; g < kPlanGroups; ++g) {
+    int x[3][K] = {};
+    if (g < p.n_groups) {
+      const PlanGroup& q = p.group[g];
+      if (q.first_page) get<K>(q.first_page, threadIdx.x, B, x[0]);
+      if (q.lost) get<K>(q.lost, threadIdx.x, B, x[1]);
+      if (q.n_freed) get<K>(q.n_freed, threadIdx.x, B, x[2]);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      first[k][g] = x[0][k];
+      lost[k][g] = x[1][k];
+      back[k][g] = x[2][k];
+    }
+  }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int b = threadIdx.x * K + k;
-    const bool in = b < B;
-    ctx[k] = in ? p.ctx_len[b] : 0;
-    const int n = in ? p.new_len[b] : 0;
+    const bool in = (int)threadIdx.x * K + k < B;
+    const int n = add[k];
     add[k] = n > 0 && n <= kMaxPos ? n : 0;   // its rows keep their place whether it is served or not
     ended[k] = n == -1;
     valid[k] = n >= -1 && n <= kMaxPos && ctx[k] >= 0 && ctx[k] <= kMaxPos - add[k];
 #pragma unroll
     for (int g = 0; g < kPlanGroups; ++g) {
-      held[k][g] = first[k][g] = lost[k][g] = back[k][g] = 0;
+      held[k][g] = 0;
       if (g >= p.n_groups || !in) continue;
       const PlanGroup& q = p.group[g];
-      if (q.first_page) first[k][g] = q.first_page[b];
-      if (q.lost) lost[k][g] = q.lost[b];
-      if (q.n_freed) back[k][g] = q.n_freed[b];
       const int f = back[k][g], most = min(q.max_pages, kMaxPos / kPage);
       valid[k] = valid[k] && f >= 0 && f <= most && lost[k][g] >= 0 && lost[k][g] <= ctx[k] - kPage * f;
       held[k][g] = ctx[k] - (lost[k][g] + kPage * f);
@@ -143,10 +176,9 @@ __global__ void __launch_bounds__(THREADS) plan_pages_kernel(const PlanArgs p) {
 
   // ---- who is served, and what comes back
   uint32_t move[4] = {0, 0, 0, 0};   // pages taken and given back, by group
-  uint32_t row_start[K];
+  uint32_t row_start[K], row_end[K], ctx_served[K], was_first[kPlanGroups][K], is_lost[kPlanGroups][K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int b = threadIdx.x * K + k;
     row_start[k] = at[0];
     at[0] += (uint32_t)add[k];
     served[k] = valid[k] && add[k] > 0 && at[0] <= (uint32_t)p.T;
@@ -155,12 +187,11 @@ __global__ void __launch_bounds__(THREADS) plan_pages_kernel(const PlanArgs p) {
       at[1 + g] += need[k][g];
       if (g < p.n_groups) served[k] = served[k] && (need[k][g] == 0 || at[1 + g] <= count[g]);
     }
-    if (b < B) {
-      field(kRowEnd)[b] = at[0];
-      field(kCtx)[b] = (uint32_t)ctx[k] * 2u + (served[k] ? 1u : 0u);
-    }
+    row_end[k] = at[0];
+    ctx_served[k] = (uint32_t)ctx[k] * 2u + (served[k] ? 1u : 0u);
 #pragma unroll
     for (int g = 0; g < kPlanGroups; ++g) {
+      was_first[g][k] = is_lost[g][k] = 0;
       if (g >= p.n_groups) continue;
       const int W = p.group[g].window;
       if (!valid[k]) back[k][g] = 0;
@@ -170,16 +201,24 @@ __global__ void __launch_bounds__(THREADS) plan_pages_kernel(const PlanArgs p) {
         to = pages_of(held[k][g]);
       else if (served[k] && W > 0)
         to = max(to, max(0, held[k][g] - W + 1) / kPage);
-      if (b < B) {
-        field(kLost0 + 4 * g)[b] = (uint32_t)now_lost;
-        field(kFirst0 + 4 * g)[b] = (uint32_t)first[k][g] | ((uint32_t)back[k][g] << 16);   // both at most 16384
-      }
+      is_lost[g][k] = (uint32_t)now_lost;
+      was_first[g][k] = (uint32_t)first[k][g] | ((uint32_t)back[k][g] << 16);   // both at most 16384
       lost[k][g] = now_lost;
       back[k][g] += to - first[k][g];
       first[k][g] = to;
       if (!served[k]) need[k][g] = 0;
       move[2 * g] += need[k][g];
       move[2 * g + 1] += (uint32_t)back[k][g];
+    }
+  }
+  if (any) {
+    put<K>(field(kRowEnd), threadIdx.x, row_end);
+    put<K>(field(kCtx), threadIdx.x, ctx_served);
+#pragma unroll
+    for (int g = 0; g < kPlanGroups; ++g) {
+      if (g >= p.n_groups) continue;
+      put<K>(field(kLost0 + 4 * g), threadIdx.x, is_lost[g]);
+      put<K>(field(kFirst0 + 4 * g), threadIdx.x, was_first[g]);
     }
   }
   uint32_t at4[4], all4[4];
@@ -189,17 +228,16 @@ __global__ void __launch_bounds__(THREADS) plan_pages_kernel(const PlanArgs p) {
   for (int g = 0; g < kPlanGroups; ++g)
     give[g] = g < p.n_groups && sound[g] && all4[2 * g + 1] <= (uint32_t)p.group[g].num_pages - count[g];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int b = threadIdx.x * K + k;
-    if (b >= B) continue;
+  for (int g = 0; g < kPlanGroups; ++g) {
+    if (g >= p.n_groups || !any) continue;
+    uint32_t take[K], given[K];
 #pragma unroll
-    for (int g = 0; g < kPlanGroups; ++g) {
-      at4[2 * g] += need[k][g];
-      at4[2 * g + 1] += (uint32_t)back[k][g];
-      if (g >= p.n_groups) continue;
-      field(kTake0 + 4 * g)[b] = at4[2 * g];
-      field(kGive0 + 4 * g)[b] = at4[2 * g + 1];
+    for (int k = 0; k < K; ++k) {
+      take[k] = at4[2 * g] += need[k][g];
+      given[k] = at4[2 * g + 1] += (uint32_t)back[k][g];
     }
+    put<K>(field(kTake0 + 4 * g), threadIdx.x, take);
+    put<K>(field(kGive0 + 4 * g), threadIdx.x, given);
   }
   __syncthreads();
   cluster_sync();   // every block has read the state: from here on it is written
@@ -391,7 +429,7 @@ cudaError_t launch(const PlanArgs& p, unsigned blocks, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = (size_t)kFields * p.B * sizeof(uint32_t);
+  cfg.dynamicSmemBytes = (size_t)kFields * ((p.B + K - 1) / K * K) * sizeof(uint32_t);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = blocks > 1 ? 2 : 1;   // (a lone block is a cluster of its own)
@@ -402,8 +440,9 @@ cudaError_t launch(const PlanArgs& p, unsigned blocks, cudaStream_t s) {
 
 cudaError_t launch_plan_pages(const PlanArgs& p, cudaStream_t s) {
   // Few requests: a small block, whose barriers are short, and one of them while its threads can take the rows in a few
-  // turns (64 decoding requests take 3.8 us, 300 mixed ones with 23 thousand rows 9.4 us, 12 with a cluster of 8). Many:
-  // two rows or pages a thread at a time (4096 requests, 105 thousand rows: 25.5 us; one 27.2, four 30.2).
+  // turns (64 decoding requests take 3.7 us, with 16 blocks 4.1, with the large block 5.2; 300 mixed ones with 32 thousand
+  // rows 8.0, with a cluster of 8 11.2). Many: two rows or pages a thread at a time (4096 requests, 110 thousand rows: 24.2
+  // us; one takes 1.6 more, four 4.5 more).
   if (p.B <= 256) return launch<1, 256, 1>(p, p.T <= 1024 ? 1 : 16, s);
   if (p.B <= 1024) return launch<1, 1024, 1>(p, 16, s);
   return launch<kPlanRequests / 1024, 1024, 2>(p, 16, s);
