@@ -508,8 +508,8 @@ g4_status g4attn_kv4_prefill(const g4attn_layer* layer, const g4attn_norms* norm
 size_t g4attn_kv4_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, int32_t max_pages,
                                          int32_t page_weights);
 
-/* g4attn_kv8_decode over a 4-bit cache (no counterpart in the RFC): arguments, fixed chunks, pos, page_weights,
- * roundings and errors as there. A request with seq_len[b] = 0 (g4attn_plan_pages writes that for one it does not
+/* g4attn_kv8_decode over a 4-bit cache (no counterpart in the RFC): arguments, fixed chunks (of 128 keys on sliding
+ * layers), pos, page_weights, roundings and errors as there. A request with seq_len[b] = 0 (g4attn_plan_pages writes that for one it does not
  * serve) holds no keys: nothing is appended for it, its row is zeros, and no error is set. The value product takes a
  * block's scale relative to the largest of its key's vector, in fp16: a block more than 2^24 below that one counts as
  * zeros there (not in the scores, and not in g4attn_kv4_prefill). */

@@ -1,7 +1,7 @@
-// Decode over the 4-bit paged cache: one query token per request, its keys split into fixed chunks (512 keys on
-// sliding layers, 1024 on global ones, aligned to key 0); inside a chunk page i goes to warp i % 4 and the warps'
-// states merge in warp order, and the chunks' states merge by a tree fixed by the chunk numbers. Every number a
-// request gets depends on its own position, window and data, and every number of a query head on that head alone.
+// Decode over the 4-bit paged cache: one query token per request, its keys split into fixed chunks (128 keys, a warp each,
+// on sliding layers; 1024 keys, four warps, on global ones; aligned to key 0); inside a global chunk page i goes to warp
+// i % 4 and the warps' states merge in warp order, and the chunks' states merge by a tree fixed by the chunk numbers. Every
+// number a request gets depends on its own position, window and data, and every number of a query head on that head alone.
 //
 // The stored codes are E2M1 with a power of two per block of 32 columns (g4_kv4.cuh). The matrix instructions
 // (m16n8k16, fp16 operands, fp32 sums) take them as fp16 numbers, one conversion per byte of two codes; the powers of
@@ -18,7 +18,7 @@
 // are fp32.
 //
 // What bounds it. Not the page stream: 64 requests of 1k to 32k keys take 365 us on a global layer (1.23 GB, 3.4 TB/s,
-// 50% of the measured copy rate) and 81 us on a sliding one (0.29 GB, 3.6 TB/s), where the 8-bit cache's decode takes
+// 50% of the measured copy rate) and 74 us on a sliding one (normed; 0.29 GB, 3.9 TB/s), where the 8-bit cache's decode takes
 // 391 and 90 for twice the bytes. A page-head block of 5456 bytes costs its warp about 1000 instructions: 256 are
 // conversions of code pairs (every global S value is needed twice, in pairs of columns for the scores and in pairs of keys
 // for the values), 64 order the keys' pairs, 64 are matrix instructions. The ALU pipe, which takes one instruction in two
@@ -29,8 +29,13 @@
 // 256 columns, with 12 warps an SM: 425; the same with two pages a step and the softmax shared out: 373 to 396; the
 // scores of page n + 1 and the values of page n in one stretch of code: 424; two pages a warp together: 414 (the loop
 // then outgrows the instruction caches). Shifts as multiplications on the other pipe: 375 to 383. Chunks of 512 keys: 436,
-// and 25 instead of 30 for a lone request of 16384. On sliding layers chunks of 256, 1024 and 2048 keys take 98, 82 and
-// 81 against 85, and a lone request of 4096 keys 15, 22 and 23 against 17.
+// and 25 instead of 30 for a lone request of 16384.
+// Sliding layers see few pages of many chunks' ends, and blocks of several warps wait for their slowest one: a warp a block
+// leaves its place to the next chunk by itself. In a graph, us for the normed mix and for a lone request of 4096 keys: 74.3
+// and 10.2; four warps to a chunk of 512 keys 80.5 and 11.0; a warp to 256 keys 73.1 and 15.4; three warps with a chunk of
+// 128 each and the queries laid out once for them 74.7. Three stages a warp in place of two 1 more; 14 or 16 blocks an SM
+// (128 registers, some spilled) no faster. Of the mix's time the copies with the blocks' starts and ends are 54, the
+// queries' norm 6 and their angles 3 (once per chunk).
 #include <atomic>
 
 #include "g4_kv4.cuh"
@@ -40,8 +45,7 @@ namespace g4 {
 
 namespace {
 
-constexpr int kChunkSliding = 512, kChunkGlobal = 1024;   // keys per chunk
-constexpr int kWarps = 4;
+constexpr int kChunkSliding = 128, kChunkGlobal = 1024;   // keys per chunk
 
 template <bool GLOBAL>
 struct Shape {
@@ -52,8 +56,9 @@ struct Shape {
   static constexpr int kQBlocks = GLOBAL ? 16 : 8;       // blocks of K's: global 12 plain, then 4 turned
   static constexpr int kHeads = GLOBAL ? 8 : 2;          // at most; columns beyond the group carry q = 0
   static constexpr int kChunk = GLOBAL ? kChunkGlobal : kChunkSliding;
-  static constexpr int kStages = GLOBAL ? 4 : 3;         // pages in flight per warp
-  static constexpr int kResident = GLOBAL ? 2 : 3;       // blocks per SM
+  static constexpr int kStages = GLOBAL ? 4 : 2;         // pages in flight per warp
+  static constexpr int kWarps = GLOBAL ? 4 : 1;          // of a chunk
+  static constexpr int kResident = GLOBAL ? 2 : 12;      // blocks per SM
   static constexpr int kStage = (Blk::kBytes + 127) / 128 * 128;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kQ = kQBlocks * 512;              // q fragments: [block][32 lanes][16 bytes]
@@ -119,10 +124,10 @@ G4_DEV uint32_t mul_f16(uint32_t a, uint32_t b) {
 }
 
 template <bool GLOBAL, bool PAGES>
-__global__ void __launch_bounds__(kWarps * 32, Shape<GLOBAL>::kResident) kv4_decode_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(Shape<GLOBAL>::kWarps * 32, Shape<GLOBAL>::kResident) kv4_decode_kernel(const ChunkParams p) {
   using S = Shape<GLOBAL>;
   using Blk = Kv4Block<GLOBAL>;
-  constexpr int D = S::D, kStages = S::kStages;
+  constexpr int D = S::D, kStages = S::kStages, kWarps = S::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* q_s = smem + S::kRing;
   uint32_t* factors = reinterpret_cast<uint32_t*>(q_s + S::kQ + (threadIdx.x >> 5) * S::kFactors);
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<GLOBAL>::kResident) kv4_dec
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, cq = lane & 3;             // matrix fragment coordinates
 
-  // This warp's query heads, warp and warp + 4, in flight while the length and the pages are looked up.
+  // This warp's query heads, warp and warp + kWarps, in flight while the length and the pages are looked up.
   constexpr int P = D / 64;   // pairs per lane: columns t0 .. t0 + P - 1 and D / 2 + t0 ..
   constexpr int kMine = (S::kHeads + kWarps - 1) / kWarps;
   const int t0 = lane * P;
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<GLOBAL>::kResident) kv4_dec
   const int k_end = min(last, c * S::kChunk + S::kChunk - 1);   // inclusive
   if (k_begin > k_end) return;                                    // unused slot
 
-  // This warp's pages: warp, warp + 4, ... of the chunk's; lane n keeps the n-th one's physical page. A
+  // This warp's pages: warp, warp + kWarps, ... of the chunk's; lane n keeps the n-th one's physical page. A
   // warp that finds one outside the pool copies none of its pages, and the chunk then adds nothing.
   const int pg0 = k_begin >> 4, n_pages = (k_end >> 4) - pg0 + 1;
   int mine = n_pages > warp ? (n_pages - warp + kWarps - 1) / kWarps : 0;   // at most 32
@@ -608,7 +613,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   }
   const long long blocks = (long long)p.NC * p.cache.hkv * p.B;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_early(kv4_decode_kernel<GLOBAL, PAGES>, (unsigned)blocks, kWarps * 32, Shape<GLOBAL>::smem(PAGES), s, p);
+  return launch_early(kv4_decode_kernel<GLOBAL, PAGES>, (unsigned)blocks, Shape<GLOBAL>::kWarps * 32, Shape<GLOBAL>::smem(PAGES), s, p);
 }
 
 int slots(bool global, int max_pages, int window) {

@@ -570,7 +570,7 @@ def test_decode_wait_that_runs_out_is_reported_and_the_next_call_is_exact():
 @pytest.mark.parametrize("kind,window", [("global", 0), ("sliding", 262144)])
 def test_decode_longest_context(kind, window):
     """262144 keys, the last usable position, against fp64 on the device. Beyond the tolerance above: the
-    sums run over 2^18 keys, in runs of 8 or 16 pages per warp and 256 or 512 chunks, each addition off by at
+    sums run over 2^18 keys, in runs of 8 or 16 pages per warp and 256 or 2048 chunks (in four sums), each addition off by at
     most 2^-24 of a partial sum that is at most sum p |v|: under 2^-15 of it in all."""
     layer = g4.global_layer() if kind == "global" else g4.sliding_layer(window)
     hkv, d, n = layer.n_kv_heads, layer.head_dim, 262144
