@@ -736,7 +736,7 @@ int32_t g4attn_provenance(const g4attn_layer* layer, char* buf, size_t len) {
                  "qrope=attention-kernel(plain),append-pass(normed,vision,exact-decode);"
                  "exact-decode=prefill-kernels-one-row-chunks;vision=image-span-per-row;"
                  "kv8=int8-pow2-step-per-token-head,split-512@abs-key0,weights:fp16-rne;"
-                 "kv4=e2m1-pow2-scale-per-32,split-512@abs-key0,weights:fp16-rne;"
+                 "kv4=e2m1-pow2-scale-per-32,split-128@abs-key0,weights:fp16-rne;"
                  "accumulator=fp32;casts=roped-q,roped-k,p,out:bf16-rne;exp=ex2.approx.ftz.f32;device=%s;dtype=bf16;"
                  "shape=Hq%d,Hkv%d,D256,W%d,theta1e4,scale%.9g;fallback=none",
                  dev, layer->n_q_heads, layer->n_kv_heads, layer->window, (double)layer->softmax_scale);

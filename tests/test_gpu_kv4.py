@@ -284,6 +284,17 @@ def test_decode_windows(window):
     s.check()
 
 
+@pytest.mark.parametrize("kind,window", [("sliding", 1024), ("sliding", 129), ("sliding", 128), ("global", 0)])
+def test_decode_around_chunk_ends(kind, window):
+    """Lengths on both sides of a chunk's end, windows that begin on both sides of one; the last chunk holds one key."""
+    lens = [127, 128, 129, 256, 257, 1023, 1025, 1151, 1152, 1153, 1154, 2049]
+    r = Rows4(kind, lens, seed=24, gap=0, **({"window": window} if window else {}))
+    r.fill()
+    s = Step4(r, weights=kind == "global")
+    s.run()
+    s.check()
+
+
 @pytest.mark.parametrize("kind", ["sliding", "global"])
 def test_decode_sharp_scores_and_blocks_of_very_different_sizes(kind):
     """Queries of size 6, values whose sizes differ by 2^13 from token to token and by 2^12 from block to block."""

@@ -224,3 +224,18 @@ def test_binding_refuses_other_types_shapes_and_strides(lib):
         g4.make_cache4(torch.zeros(4, 8, dtype=torch.uint8).t(), 1)
     with pytest.raises(ctypes.ArgumentError):                  # an 8-bit cache is not a 4-bit one
         lib.g4attn_kv4_append(L(S), None, 16, 16, 8, 16, 16, 16, 1, L(g4.g4attn_cache8(16, 4, 16)), 16, 1, None)
+
+
+@pytest.mark.parametrize("tp", [1, 2])
+def test_provenance_names_the_chunks_that_the_workspace_holds(lib, tp):
+    """The record's split is the one the decode makes: a state of D + 2 floats per head and chunk slot, in two runs of
+    whole 256 bytes."""
+    for layer, window in ((g4.sliding_layer(tp=tp), 1024), (g4.sliding_layer(700, tp=tp), 700), (g4.global_layer(tp=tp), 0)):
+        chunk = int(g4.g4attn_provenance(layer).split("kv4=")[1].split("split-")[1].split("@")[0])
+        d, width = layer.head_dim, 1000
+        slots = -(-width * 16 // chunk)
+        if window:
+            slots = min(slots, (window - 1) // chunk + 2)
+        states = 3 * layer.n_q_heads * slots
+        want = sum(-(-states * 4 * n // 256) * 256 for n in (2, d))
+        assert g4.g4attn_kv4_decode_workspace_bytes(layer, 3, width) == want
