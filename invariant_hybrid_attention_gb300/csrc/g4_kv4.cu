@@ -79,8 +79,11 @@ G4_DEV void store_line(const Line* line, uint8_t* tile, uint8_t* scales, uint8_t
 
 // A sliding row's heads arrive through shared memory, two heads of K' and V (64 bytes a lane) to a stage, one stage ahead
 // of their use: a warp that held them in registers had its loads in flight for the codes' arithmetic alone, and waited
-// for them (4 x 4096 rows: 85 us, 70 so; two stages ahead, with fewer blocks an SM, 78).
-constexpr int kAhead = 1, kAppendStages = kAhead + 1, kAppendWarps = 4;
+// for them (4 x 4096 rows: 85 us, 70 so; two stages ahead 2.8 more).
+constexpr int kAhead = 1, kAppendStages = kAhead + 1;
+// A warp a block: it leaves its place to the next row by itself (96 and 200 rows with their read-back: 10.0 us in a graph,
+// blocks of four warps 11.6; 4 x 4096: 120.1 and 122.5; 28 blocks an SM, of 72 registers, 125.6).
+constexpr int kAppendWarps = 1, kAppendBlocks = 24;
 
 G4_DEV void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -108,10 +111,11 @@ struct AppendArgs {
 // One warp per (row, share of the KV heads). The row's angles are computed once for its heads, in two-part
 // arithmetic. Sliding: half a warp per vector, two heads at a time, K' then V. Global: a warp per head for S, then
 // 8 lanes per head for the turned columns of up to four heads at once.
-// The 4 x 4096 sliding rows take 70 us (340 MB, 4.8 TB/s, 72% of the copy rate; the ALU pipe 55%, 2.9 instructions a
-// cycle), the 2 x 8192 global ones 37 us timed by events, some 6 of which an empty stretch reads too (89 MB).
+// The 4 x 4096 sliding rows take 70 us with cold caches in blocks of four warps (340 MB, 4.8 TB/s, 72% of the copy rate; the
+// ALU pipe 55%, 2.9 instructions a cycle) and 2 less in blocks of one, the 2 x 8192 global ones 33 us timed by events, some
+// 6 of which an empty stretch reads too (89 MB).
 template <bool GLOBAL, bool NORM, int MODE>
-__global__ void __launch_bounds__(kAppendWarps * 32, 6) kv4_append_kernel(const AppendArgs p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendBlocks) kv4_append_kernel(const AppendArgs p) {
   using Blk = Kv4Block<GLOBAL>;
   constexpr int D = Blk::D, R = Blk::R, LPV = D / 16;
   __shared__ __align__(16) float2 angles[kAppendWarps][R];
@@ -242,26 +246,30 @@ G4_DEV uint4 eight_bf16(uint32_t lo16, uint32_t hi16, float factor) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Bound by its loads: the 4 x 4096 sliding rows take 54 us (56 with cold caches; 340 MB, 6.1 to 6.3 TB/s).
+// Bound by its loads: the 4 x 4096 sliding rows take 54 us (56 with cold caches; 340 MB, 6.1 to 6.3 TB/s). Blocks of four
+// warps, eight an SM and two rounds of them: against blocks of eight warps, 0.5 us less for small calls, the same for large
+// ones; blocks of one warp 1 us less for the large call and 6 more for 64 single rows, many warps looking for few pages.
+constexpr int kUnpackWarps = 4, kUnpackBlocks = 8;
+
 // One warp per (page, KV head), walking the batch's pages in a grid-sized stride. Lane (key kk = lane & 7, q = lane
 // >> 3) turns columns 8q .. 8q + 7 of every block of its key into core-matrix rows, so a warp store fills four whole
 // 128-byte core matrices.
 template <bool GLOBAL>
-__global__ void __launch_bounds__(256, 4) kv4_unpack_kernel(const UnpackArgs p) {
+__global__ void __launch_bounds__(kUnpackWarps * 32, kUnpackBlocks) kv4_unpack_kernel(const UnpackArgs p) {
   using Blk = Kv4Block<GLOBAL>;
   constexpr int D = Blk::D;
   wait_for_grid();
   let_next_grid_start();
   const int lane = threadIdx.x & 31;
   const int HKV = p.src.hkv;
-  const long long stride = (long long)gridDim.x * 8;
+  const long long stride = (long long)gridDim.x * kUnpackWarps;
   // A prefill's attention multiplies the slots before a window's first key, in its page, by zero: they
   // are set to zero, since anything else might not be a number.
   const bool zero_before = p.range.key_begin == nullptr;
   const int kk = lane & 7, q = lane >> 3;
   long long base = 0;   // units before sequence group b0
   int b0 = 0;
-  for (long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);; unit += stride) {
+  for (long long unit = (long long)blockIdx.x * kUnpackWarps + (threadIdx.x >> 5);; unit += stride) {
     int lo, hi, page, g, from, to;
     const int found = find_page(p, unit, lane, base, b0, lo, hi, page, g, from, to);
     if (found < 0) return;
@@ -358,9 +366,10 @@ cudaError_t launch_kv4_unpack(bool global, const Kv8Range& range, const PagedCac
   if (range.rows.B <= 0) return cudaSuccess;
   UnpackArgs a{range, src, dst, st.err};
   const long long units = (long long)range.rows.B * src.max_pages * src.hkv;   // at most
-  const unsigned blocks = (unsigned)(units + 7 < 8LL * 152 * 8 ? (units + 7) / 8 : 152 * 8);
-  return global ? launch_early(kv4_unpack_kernel<true>, blocks, 256, 0, s, a)
-                : launch_early(kv4_unpack_kernel<false>, blocks, 256, 0, s, a);
+  const long long some = (units + kUnpackWarps - 1) / kUnpackWarps;
+  const unsigned blocks = (unsigned)(some < 152 * 2 * kUnpackBlocks ? some : 152 * 2 * kUnpackBlocks);
+  return global ? launch_early(kv4_unpack_kernel<true>, blocks, kUnpackWarps * 32, 0, s, a)
+                : launch_early(kv4_unpack_kernel<false>, blocks, kUnpackWarps * 32, 0, s, a);
 }
 
 }  // namespace g4
