@@ -552,9 +552,10 @@ typedef struct {
   const int32_t* lost;        /* [B] or NULL, window 0 only: keys that a request lost to evictions */
   int32_t* out_lost;          /* [B]: the same after the step; may be lost */
   const int32_t* freed;       /* [B][max_pages] and */
-  const int32_t* n_freed;     /* [B], or both NULL: the pages of the latest g4attn_evict_pages; with lost */
+  const int32_t* n_freed;     /* [B]: the pages of the latest g4attn_evict_pages; with lost and out_n_freed, or NULL */
   int32_t* seq_len;           /* [B] out: held keys, new ones included, of the served requests; 0 of the others */
   int64_t* slots;             /* [T] out, or NULL: 16 * physical page + place in the page of each row's key; -1 for none */
+  int32_t* out_n_freed;       /* [B], with n_freed: 0 where the step took the pages back; may be n_freed */
 } g4attn_page_group;
 
 /* Plans one serving step on the device (the RFC has no counterpart): who is served, the page tables, and the rows'
@@ -568,7 +569,9 @@ typedef struct {
  *   A served request gets q_len[b] = new_len[b], out_ctx_len[b] = ctx_len[b] + new_len[b], its new pages in the table
  *   (the j-th page that the step takes is the ring's j-th free one) and, in a group with a window, gives back the
  *   pages wholly before its first new row's window. A request that has ended gives back all its pages, and its
- *   ctx_len, first_page and lost become 0. The pages in freed come back too, and lost grows by 16 for each.
+ *   ctx_len, first_page and lost become 0. The pages in freed come back too, and lost grows by 16 for each: a step
+ *   takes them once and writes 0 to out_n_freed, so a later step without an eviction between has to read its n_freed
+ *   there (with out_n_freed = n_freed it does). A request that is refused keeps its pages in the list.
  *   Pages come back behind the ring's end, in the requests' order (a request's evicted ones first), and can be taken
  *   from the next step on. Table entries of pages given back are left as they are; no call reads them.
  * ctx_start[b] = ctx_len[b]. positions, [T] or NULL: each row's RoPE position; -1 for rows of no request, those behind

@@ -68,7 +68,7 @@ class g4attn_cache4(ctypes.Structure):
 class g4attn_page_group(ctypes.Structure):
     _fields_ = [("window", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)] + [
         (name, ctypes.c_void_p) for name in ("free_pages", "pool", "out_pool", "page_table", "first_page", "out_first_page",
-                                             "lost", "out_lost", "freed", "n_freed", "seq_len", "slots")]
+                                             "lost", "out_lost", "freed", "n_freed", "seq_len", "slots", "out_n_freed")]
     tensors = None   # make_page_group: what the fields point into
     room = None      # its requests, rows (None: no slots) and device
 
@@ -646,15 +646,20 @@ def g4attn_kv4_decode(layer, norms, q, k_new, v_new, seq_len, cache: g4attn_cach
 # ---- the page plan --------------------------------------------------------------------------------------
 
 def make_page_group(window: int, page_table, free_pages, pool, out_pool, seq_len, slots=None, first_page=None,
-                    out_first_page=None, lost=None, out_lost=None, freed=None, n_freed=None) -> g4attn_page_group:
+                    out_first_page=None, lost=None, out_lost=None, freed=None, n_freed=None,
+                    out_n_freed=None) -> g4attn_page_group:
     """One layer kind's pages (window 0: a global one), as int32 tensors (slots: int64) on one device that the group
     keeps. page_table [B, columns], free_pages [physical pages], pool [2]; slots [T]; the others [B] (freed as
-    page_table)."""
+    page_table). out_n_freed None: n_freed itself where out_lost is lost, so that the pages of an eviction come back once;
+    else an array of the group's own, group.tensors["out_n_freed"], which is the n_freed of the state in out_lost."""
     import torch
     B, width = page_table.shape
+    if n_freed is not None and out_n_freed is None:
+        in_place = lost is not None and out_lost is not None and lost.data_ptr() == out_lost.data_ptr()
+        out_n_freed = n_freed if in_place else torch.zeros_like(n_freed)
     tensors = dict(free_pages=free_pages, pool=pool, out_pool=out_pool, page_table=page_table, first_page=first_page,
                    out_first_page=out_first_page, lost=lost, out_lost=out_lost, freed=freed, n_freed=n_freed,
-                   seq_len=seq_len, slots=slots)
+                   seq_len=seq_len, slots=slots, out_n_freed=out_n_freed)
     shapes = dict(free_pages=(free_pages.numel(),), pool=(2,), out_pool=(2,), page_table=(B, width), freed=(B, width),
                   slots=(None if slots is None else slots.numel(),))
     for name, t in tensors.items():

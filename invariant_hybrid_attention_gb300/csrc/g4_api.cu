@@ -684,13 +684,15 @@ g4_status g4attn_plan_pages(const int32_t* ctx_len, const int32_t* new_len, int3
     if (!g.free_pages || !g.pool || !g.out_pool || !g.page_table || !g.seq_len) return G4_ERR_INVALID;
     if ((g.window > 0) != (g.first_page != nullptr) || (g.first_page != nullptr) != (g.out_first_page != nullptr))
       return G4_ERR_INVALID;
-    if ((g.lost != nullptr) != (g.out_lost != nullptr) || (g.freed != nullptr) != (g.n_freed != nullptr))
+    if ((g.lost != nullptr) != (g.out_lost != nullptr) || (g.freed != nullptr) != (g.n_freed != nullptr) ||
+        (g.n_freed != nullptr) != (g.out_n_freed != nullptr))
       return G4_ERR_INVALID;
     if (g.window > 0 ? g.lost != nullptr || g.freed != nullptr : g.freed != nullptr && g.lost == nullptr)
       return G4_ERR_INVALID;
     if (reinterpret_cast<uintptr_t>(g.slots) & 7u) return G4_ERR_INVALID;
     p.group[i] = PlanGroup{g.window, g.num_pages, g.max_pages, g.free_pages, g.pool, g.out_pool, g.page_table,
-                           g.first_page, g.out_first_page, g.lost, g.out_lost, g.freed, g.n_freed, g.seq_len, g.slots};
+                           g.first_page, g.out_first_page, g.lost, g.out_lost, g.freed, g.n_freed, g.seq_len, g.slots,
+                           g.out_n_freed};
   }
   p.ctx_len = ctx_len;
   p.new_len = new_len;

@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(THREADS) plan_pages_kernel(const PlanArgs p) {
         q.seq_len[b] = served[k] ? held[k][g] + add[k] : 0;
         if (q.out_first_page) q.out_first_page[b] = gone ? 0 : first[k][g];
         if (q.out_lost) q.out_lost[b] = gone ? 0 : lost[k][g];
+        if (q.out_n_freed) q.out_n_freed[b] = valid[k] ? 0 : q.n_freed[b];   // its pages come back once
       }
     }
   }

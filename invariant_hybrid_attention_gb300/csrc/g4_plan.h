@@ -23,6 +23,7 @@ struct PlanGroup {
   const int32_t* n_freed;
   int32_t* seq_len;
   int64_t* slots;
+  int32_t* out_n_freed;
 };
 
 struct PlanArgs {

@@ -456,3 +456,60 @@ def test_a_serving_loop_of_plan_prefill_decode_and_eviction(captured):
         if k == "global":
             pages += [p for b in range(n) for p in freed[b, :int(n_freed[b])].tolist()]
         assert sorted(pages) == list(range(pools[k])), k
+
+
+# ---- evictions between steps -----------------------------------------------------------------------------
+
+def census(d, p):
+    """Every physical page of the first group, from where it is: free, held, or evicted and not yet taken back."""
+    x, (h, c) = d["groups"][0], d["groups"][0]["out_pool"].tolist()
+    n = p.groups[0]["num_pages"]
+    pages = [int(x["ring"][(h + i) % n]) for i in range(c)]
+    for b, tokens in enumerate(d["out_ctx"].tolist()):
+        pages += x["table"][b, :oplan.pages(tokens - int(x["out_lost"][b]))].tolist()
+    return sorted(pages)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_pages_of_an_eviction_come_back_once(captured):
+    """Steps without an eviction between them, in place: the first takes the evicted pages back, the others none."""
+    p = Plan([200, 400, 60, 80], [1, 1, 1, 1], 6, windows=(0,), spare=12, evicted=True, seed=2, width=30)
+    assert any(p.groups[0]["freed"])
+    d, twin = p.device(in_place=True), p.device(in_place=True)
+    p.call(twin)                                             # the library's first call comes before any capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    if captured:
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            p.call(d)
+    for _ in range(4):
+        graph.replay() if captured else p.call(d)
+        status_ok()
+        p.check(d)
+        assert d["groups"][0]["n_freed"].tolist() == [0, 0, 0, 0]
+        assert census(d, p) == list(range(p.groups[0]["num_pages"]))
+        groups = copy.deepcopy(p.groups)
+        p.ctx, *_ = oplan.plan(p.ctx, p.new, p.rows, groups)
+        groups[0]["freed"] = [[] for _ in p.ctx]
+        p.groups = groups
+
+
+def test_pages_of_an_eviction_that_a_step_does_not_take_stay_in_their_list():
+    """Outputs apart from the inputs; a request that is refused, one that waits, one that ends."""
+    p = Plan([200, 400, 160, 280], [1, 1, 300, -1], 400, windows=(0,), spare=8, evicted=True, seed=3, width=60)
+    counts = [len(f) for f in p.groups[0]["freed"]]
+    assert all(counts)
+    d = p.device()
+    x = d["groups"][0]
+    p.call(d)
+    status_ok()
+    assert p.check(d)[2] == 0                                  # short of pages: its evicted ones come back all the same
+    assert x["n_freed"].tolist() == counts and x["group"].tensors["out_n_freed"].tolist() == [0, 0, 0, 0]
+    d = p.device()
+    d["ctx"][1] = -1
+    x = d["groups"][0]
+    p.call(d)
+    torch.cuda.synchronize()
+    assert g4.g4attn_status_sync() == g4.G4_ERR_DEVICE
+    assert x["group"].tensors["out_n_freed"].tolist() == [0, counts[1], 0, 0]
+    assert int(x["out_lost"][1]) == int(x["lost"][1])

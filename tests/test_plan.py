@@ -99,3 +99,32 @@ def test_binding_refuses_other_types_shapes_and_sizes(lib):
     for name, bad in (("new_len", z(4)), ("q_len", z(3, t=torch.int64)), ("positions", z(18)[::2])):
         with pytest.raises(ValueError, match=name):
             g4.g4attn_plan_pages(**{**a, name: bad})
+
+
+def test_the_freed_pages_come_with_a_place_for_their_count_after_the_step(lib):
+    """A list of evicted pages that no step marks as taken would come back at every step."""
+    I = g4.G4_ERR_INVALID
+    names = [name for name, _ in g4.g4attn_page_group._fields_]
+
+    def call(**kw):
+        g = group()
+        for name, value in kw.items():
+            assert name in names
+            setattr(g, name, value)
+        a = (g4.g4attn_page_group * 1)(g)
+        return lib.g4attn_plan_pages(16, 16, 2, 8, a, 1, 16, 16, 16, 16, 16, None)
+    lost = dict(lost=16, out_lost=16)
+    assert call(**lost, freed=16, n_freed=16) == I
+    assert call(**lost, out_n_freed=16) == I and call(out_n_freed=16) == I
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t)   # noqa: E731
+    a = dict(window=0, page_table=z(3, 5), free_pages=z(20), pool=z(2), out_pool=z(2), seq_len=z(3), freed=z(3, 5),
+             n_freed=torch.ones(3, dtype=torch.int32), lost=z(3))
+    inside = g4.make_page_group(**a, out_lost=a["lost"])
+    assert inside.out_n_freed == inside.n_freed == a["n_freed"].data_ptr()
+    apart = g4.make_page_group(**a, out_lost=z(3))
+    kept = apart.tensors["out_n_freed"]
+    assert apart.out_n_freed == kept.data_ptr() != apart.n_freed and kept.shape == (3,)
+    given = z(3)
+    assert g4.make_page_group(**a, out_lost=z(3), out_n_freed=given).out_n_freed == given.data_ptr()
+    with pytest.raises(ValueError, match="out_n_freed"):
+        g4.make_page_group(**a, out_lost=z(3), out_n_freed=z(4))
