@@ -509,10 +509,10 @@ size_t g4attn_kv4_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, i
                                          int32_t page_weights);
 
 /* g4attn_kv8_decode over a 4-bit cache (no counterpart in the RFC): arguments, fixed chunks (of 128 keys on sliding
- * layers), pos, page_weights, roundings and errors as there. A request with seq_len[b] = 0 (g4attn_plan_pages writes that for one it does not
- * serve) holds no keys: nothing is appended for it, its row is zeros, and no error is set. The value product takes a
- * block's scale relative to the largest of its key's vector, in fp16: a block more than 2^24 below that one counts as
- * zeros there (not in the scores, and not in g4attn_kv4_prefill). */
+ * layers), pos, page_weights, roundings and errors as there. A request with seq_len[b] = 0 (g4attn_plan_pages writes
+ * that for one it does not serve) holds no keys: nothing is appended for it, its row is zeros, and no error is set. The
+ * value product takes a block's scale relative to the largest of its key's vector, in fp16: a block more than 2^24 below
+ * that one counts as zeros there (not in the scores, and not in g4attn_kv4_prefill). */
 g4_status g4attn_kv4_decode(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k_new,
                             const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B,
                             const g4attn_cache4* cache, const int32_t* page_table, int32_t max_pages,
@@ -575,8 +575,19 @@ typedef struct {
  *   Pages come back behind the ring's end, in the requests' order (a request's evicted ones first), and can be taken
  *   from the next step on. Table entries of pages given back are left as they are; no call reads them.
  * ctx_start[b] = ctx_len[b]. positions, [T] or NULL: each row's RoPE position; -1 for rows of no request, those behind
- * the last one among them. So q_start, q_len, ctx_start and a group's page_table are what a prefill takes; a decode
- * step of new_len 1 for every request takes seq_len, page_table and (where keys were lost) positions as pos.
+ * the last one among them.
+ * What the other calls take of a plan:
+ *   a prefill    q_start, q_len, ctx_start and a group's page_table.
+ *   a decode     (new_len at most 1; q, k_new, v_new and out by request, not by row) a group's seq_len and page_table,
+ *                and ctx_start as pos: the position of the request's one new row, whatever keys it lost. positions is
+ *                no pos: it goes by rows, and shifts against the requests where one without rows lies before another.
+ *                Of the decodes only g4attn_kv4_decode takes seq_len = 0 for a request without rows; the bf16 and the
+ *                8-bit ones report it (G4_ERR_DEVICE) in every step that holds such a request.
+ *   a step of prompts and decoding requests is two plans: new_len 0 for the prompts, then the decode; new_len 0 for the
+ *                decoding requests, then the prefill.
+ *   a request that lost keys goes on by rows of new_len 1: no prefill turns its rows by their positions.
+ *   an eviction  the held keys of all requests, out_ctx_len - out_lost, not seq_len: that is 0 for a request that is
+ *                only idle in this step, and an eviction empties the table of a request of length 0.
  * out_ctx_len, q_len and ctx_start may be ctx_len or new_len's arrays, as long as no two outputs are one; two groups
  * share no array. A captured call can be replayed. The plan knows no image spans: the pages of an image that began
  * before its chunk's window are not kept for it. 1 <= B <= 4096, T >= 0.

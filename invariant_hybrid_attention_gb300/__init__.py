@@ -678,7 +678,8 @@ def make_page_group(window: int, page_table, free_pages, pool, out_pool, seq_len
 
 def g4attn_plan_pages(ctx_len, new_len, groups, out_ctx_len, q_start, q_len, ctx_start, positions, stream=None):
     """Plans one serving step of B requests and T = len(positions) rows over one or two page groups: who is served,
-    page tables, slots, positions. out_ctx_len may be ctx_len."""
+    page tables, slots, positions. out_ctx_len may be ctx_len. A prefill takes q_start, q_len and ctx_start;
+    g4attn_kv4_decode a group's seq_len, and ctx_start as pos (positions goes by rows, pos by requests)."""
     _, i32, _, _, _ = _names or _torch_names()
     B, T, n = ctx_len.shape[0], positions.shape[0], len(groups)
     rows = (B,)

@@ -513,3 +513,118 @@ def test_pages_of_an_eviction_that_a_step_does_not_take_stay_in_their_list():
     assert g4.g4attn_status_sync() == g4.G4_ERR_DEVICE
     assert x["group"].tensors["out_n_freed"].tolist() == [0, counts[1], 0, 0]
     assert int(x["out_lost"][1]) == int(x["lost"][1])
+
+
+def test_a_step_of_prompts_decoding_and_idle_requests():
+    """Two plans a step, one for the decoding requests and one for the prompts, as the calls that follow want them. Slot 0
+    is empty at first, slot 1 decodes and loses pages to evictions, slot 2 gets its prompt in two chunks and then
+    decodes, slot 3 decodes in every other step only. Every decode row against fp64 over the keys that the request must
+    hold by then, at its own position."""
+    window, n, width = 32, 4, 16
+    kinds = ("global", "sliding")
+    layers = {k: make_layers(k, window) for k in kinds}
+    pools = {"global": 40, "sliding": 30}
+    cache = {k: PagedKV4(layers[k][0], pools[k]) for k in kinds}
+    scratch = {k: PagedKV(pools[k], layers[k][0].n_kv_heads, layers[k][0].head_dim, k == "global") for k in kinds}
+    z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device="cuda")   # noqa: E731
+    table = {k: torch.full((n, width), -1, dtype=torch.int32, device="cuda") for k in kinds}
+    ring = {k: torch.randperm(pools[k], device="cuda").int() for k in kinds}
+    pool = {k: i32([0, pools[k]]) for k in kinds}
+    seq = {k: z(n) for k in kinds}
+    first, lost, freed, n_freed, ctx = z(n), z(n), z(n, width), z(n), z(n)
+    weights = torch.zeros(n, width, device="cuda")
+    ws = {k: workspace(layers[k][0], n, width, k == "global") for k in kinds}
+    held, seed = [{k: None for k in kinds} for _ in range(n)], [0]
+
+    def normal(*shape):
+        seed[0] += 1
+        return gi.bf16_normal(shape, seed[0]).cuda()
+
+    def plan(new):
+        rows = sum(max(0, x) for x in new)
+        x = dict(pos=z(rows), start=z(n), len=z(n), ctx=z(n), slots={k: z(rows, t=torch.int64) for k in kinds})
+        g = [g4.make_page_group(0, table["global"], ring["global"], pool["global"], pool["global"], seq["global"],
+                                x["slots"]["global"], lost=lost, out_lost=lost, freed=freed, n_freed=n_freed),
+             g4.make_page_group(window, table["sliding"], ring["sliding"], pool["sliding"], pool["sliding"],
+                                seq["sliding"], x["slots"]["sliding"], first_page=first, out_first_page=first)]
+        g4.g4attn_plan_pages(ctx, i32(new), g, ctx, x["start"], x["len"], x["ctx"], x["pos"])
+        status_ok()
+        assert x["len"].tolist() == [max(0, v) for v in new]
+        return x
+
+    def keep(k, b, slots):
+        got = [v[slots // 16, :, slots % 16].double().cpu().numpy() for v in untile4(cache[k].pages, layers[k][0].head_dim)]
+        old = held[b][k]
+        held[b][k] = got if old is None else [np.concatenate([h, x]) for h, x in zip(old, got)]
+
+    def kv(k, rows):
+        layer = layers[k][0]
+        shape = (rows, layer.n_kv_heads, layer.head_dim)
+        return normal(*shape), normal(*shape) if k == "sliding" else None
+
+    def prefill(new):
+        x = plan(new)
+        for k in kinds:
+            layer = layers[k][0]
+            q = normal(sum(max(0, v) for v in new), 32, layer.head_dim)
+            g4.g4attn_kv4_prefill(layer, None, q, *kv(k, q.shape[0]), x["start"], x["len"], x["ctx"], cache[k].desc, table[k],
+                                  scratch[k].desc, table[k], torch.empty_like(q))
+            status_ok()
+            for b in range(n):
+                if new[b] > 0:
+                    at = int(x["start"][b])
+                    keep(k, b, x["slots"][k][at:at + new[b]])
+
+    def decode(new):
+        x = plan(new)
+        for k in kinds:
+            layer, ol = layers[k]
+            q = normal(n, 32, layer.head_dim)
+            out = torch.full_like(q, float("nan"))
+            g4.g4attn_kv4_decode(layer, None, q, *kv(k, n), seq[k], cache[k].desc, table[k], out, ws[k], pos=x["ctx"] if
+                                 k == "global" else None, page_weights=weights if k == "global" else None)
+            status_ok()
+            for b in range(n):
+                if new[b] != 1:
+                    assert (out[b] == 0).all()
+                    continue
+                at = int(x["start"][b])
+                keep(k, b, x["slots"][k][at:at + 1])
+                position = int(x["ctx"][b])
+                assert int(x["pos"][at]) == position
+                mine = [h[-window:] for h in held[b][k]] if k == "sliding" else held[b][k]
+                kk, vv = kv8.keys_values(ol, *mine)
+                roped, steps = turned_queries(ol, q[b:b + 1], [position])
+                want, _, mag, peak = kv8.decode(roped[0], kk, vv, layer.softmax_scale)
+                assert_row(f64(out[b]), want, mag, peak, border(steps[0], kk, layer.softmax_scale))
+
+    def evict(pages):
+        before, length = table["global"].tolist(), ctx - lost
+        g4.g4attn_evict_pages(length, table["global"], weights, pages, 1, 1, z(n), table["global"], weights, freed, n_freed)
+        status_ok()
+        after, cut = table["global"].tolist(), n_freed.tolist()
+        for b, m in enumerate(length.tolist()):
+            if m:
+                kept = after[b][:oplan.pages(m) - cut[b]]
+                idx = np.concatenate([np.arange(16 * i, min(16 * i + 16, m)) for i in range(oplan.pages(m))
+                                      if before[b][i] in kept])
+                held[b]["global"] = [h[idx] for h in held[b]["global"]]
+        return cut
+
+    prefill([0, 100, 0, 70])
+    for step in range(24):
+        decode([1 if step > 15 else 0, 1, 1 if step > 10 else 0, step % 2])
+        if step in (4, 10):
+            prefill([0, 0, 45 if step == 4 else 20, 0])
+        if step == 15:
+            prefill([33, 0, 0, 0])
+        if step in (6, 17):                                   # slot 3 is idle or not; it keeps its pages either way
+            assert evict(4)[1] > 0
+    assert int(lost[1]) > 0 and ctx.tolist() == [41, 124, 78, 82]
+    for k in kinds:
+        h, c = pool[k].tolist()
+        pages = [int(ring[k][(h + i) % pools[k]]) for i in range(c)]
+        for b in range(n):
+            m = int(ctx[b]) - (int(lost[b]) if k == "global" else 0)
+            pages += table[k][b, (int(first[b]) if k == "sliding" else 0):oplan.pages(m)].tolist()
+        assert sorted(pages) == list(range(pools[k])), k
