@@ -510,9 +510,12 @@ size_t g4attn_kv4_decode_workspace_bytes(const g4attn_layer* layer, int32_t B, i
 
 /* g4attn_kv8_decode over a 4-bit cache (no counterpart in the RFC): arguments, fixed chunks (of 128 keys on sliding
  * layers), pos, page_weights, roundings and errors as there. A request with seq_len[b] = 0 (g4attn_plan_pages writes
- * that for one it does not serve) holds no keys: nothing is appended for it, its row is zeros, and no error is set. The
- * value product takes a block's scale relative to the largest of its key's vector, in fp16: a block more than 2^24 below
- * that one counts as zeros there (not in the scores, and not in g4attn_kv4_prefill). */
+ * that for one it does not serve) holds no keys: nothing is appended for it, its row is zeros, and no error is set. In the
+ * value product a key's weight for a block of V's columns is p_j 2^E_jb in fp16, p_j the softmax weight and 2^E_jb the
+ * block's scale, held against the largest such number P of all keys and blocks that the row sees: it is off by at most
+ * 2^-11 of itself while it is at least 2^-21 P, by 2^-31 P below that, and may count as zero from 2^-32 P down. So a
+ * block far smaller than one of another key can add nothing even in columns where that other key holds zeros
+ * (g4attn_kv4_prefill casts p_j alone, to bf16, and has no such limit). */
 g4_status g4attn_kv4_decode(const g4attn_layer* layer, const g4attn_norms* norms, const void* q, const void* k_new,
                             const void* v_new, const int32_t* seq_len, const int32_t* pos, int32_t B,
                             const g4attn_cache4* cache, const int32_t* page_table, int32_t max_pages,

@@ -8,12 +8,15 @@
 // two stay outside:
 //   scores   x_j = scale log2(e) sum over blocks 2^s_jb (c_jb . q_b): a block is two matrix steps into sums of their
 //            own, which join the score times 2^(s_jb - 167) (the 2^-40 keeps every scale in fp32's range). q is fp16
-//            scaled by a power of two per head: the bf16 q' is exact there, down to 2^-38 of its largest magnitude;
+//            scaled by a power of two per head, its largest magnitude at 2^14: the bf16 q' is exact there down to 2^-31
+//            of that magnitude, where fp16's smallest step passes its eighth bit, and at most 2^-39 of it off below;
 //   weights  P.V needs w_jb = p_j 2^s_jb for every block b of V's columns. w_j = 2^(x_j + top_j - m2 + 7) in fp16, top_j
 //            the key's largest scale, with a running maximum m2 of x_j + top_j of its own, apart from the maximum m1
 //            that the sum of p_j = 2^(x_j - m1) is kept with; a block's weight is w_j 2^(s_jb - top_j), an exact fp16
-//            product while it does not fall below 2^-14 (2^-29 of the largest weight). A head's m2 moves only when its
-//            own maximum grows by more than 2^8, so w_j <= 2^15.
+//            product while it does not fall below 2^-14. A head's m2 moves only when its own maximum grows by more than
+//            2^8, so the largest w_j so far is between 2^7 and 2^15: weights are exact but for the cast of w_j down to
+//            2^-21 of the row's largest p_j 2^top_j (over all its keys), below that each of the two roundings is at
+//            most 2^-25 beside 2^7, 2^-32 of the largest, and what is smaller than that is lost.
 // Declared roundings: roped q to bf16, w to fp16 (2^-11 relative, each weight by itself), the output to bf16; all sums
 // are fp32.
 //

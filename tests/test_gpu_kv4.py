@@ -782,3 +782,36 @@ def test_wrong_device_and_strides_are_refused():
         g4.g4attn_kv4_decode(r.layer, None, s.q, None, None, i32([40]), r.cache.desc, r.table, s.out, s.ws.cpu())
     with pytest.raises(g4.G4Error):
         g4.g4attn_kv4_decode(r.layer, None, s.q, None, None, i32([40]), r.cache.desc, r.table, s.out, s.ws[:64])
+
+
+@pytest.mark.parametrize("power", [8, 12, 20, 24, 26, 32, 40])
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_decode_beside_one_key_with_one_large_block(kind, power):
+    """A key with a block 2^power larger than all others and zeros elsewhere: what the other blocks' columns keep. The
+    limit is the header's, for each of n keys: 2^-31 of the row's largest p 2^E times a code of at most 6, where the
+    largest |v| of a key is at least 4 * 2^E. Up to 2^16 every weight, p within 2 of the largest and a block of 32 normal
+    numbers within 2^3 of another, is at least 2^-20 of that largest, and only its cast is left (2^-11 of each)."""
+    r = Rows4(kind, [300, 1500], seed=35, gap=0)
+    for x in (r.v if kind == "sliding" else r.k):
+        x[7] = 0
+        x[7, :, 128:160] = (r.q[0][0, 0, :32].double() * 2.0 ** power).bfloat16()
+    r.fill()
+    s = Step4(r, q_scale=2.0 ** -12)                     # scores next to 0: all weights alike
+    s.q[..., 128:160] = 0                                # (a global key is its value too)
+    s.run()
+    status_ok()
+    q, steps = turned_queries(r.olayer, s.q, s.pos)
+    scale, got = r.layer.softmax_scale, f64(s.out)
+    others = np.setdiff1d(np.arange(r.layer.head_dim), np.arange(128, 160))
+    for b, n in enumerate(s.lens):
+        k, v = kv8.keys_values(r.olayer, *r.values(b))
+        lo = max(0, n - r.layer.window) if kind == "sliding" else 0
+        want, p, mag, peak = kv8.decode(q[b], k, v, scale, lo)
+        assert p[:, lo:].min() * 2 > p.max()
+        seen = lo <= 7
+        lost = 1.5 * 2.0 ** -31 * peak if seen and power > 16 else 0
+        limit = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -16 + border(steps[b], k, scale)) * mag + lost
+        if seen and 16 < power < 25:                     # the limit says something in these columns
+            assert np.median(limit[:, others]) < np.median(mag[:, others])
+        over = np.abs(got[b] - want) - limit
+        assert (over <= 0).all(), (b, over.max())
