@@ -815,3 +815,50 @@ def test_decode_beside_one_key_with_one_large_block(kind, power):
             assert np.median(limit[:, others]) < np.median(mag[:, others])
         over = np.abs(got[b] - want) - limit
         assert (over <= 0).all(), (b, over.max())
+
+
+def normed_turned_queries(r, q, pos):
+    """Normed queries as the definition casts and turns them, in fp64, and per column the step to the neighbour it may be
+    instead. Before the first cast the kernel's fp32 x is off by at most 2^-20 of itself (a sum of 512 squares over 32
+    lanes, half of whose 21 roundings the root keeps, then the root, a quotient and two products); a column next to a
+    border of that cast moves its pair's turned columns by a step too, and plain columns are turned by nothing."""
+    norms = r.norms.oracle
+    x = oracle.normed_q(norms, q.double().cpu().numpy())
+    d, turned = x.shape[-1], kv8.turned_columns(r.olayer)
+    plain = np.setdiff1d(np.arange(d), turned)
+    if r.kind == "global":
+        x[..., plain] *= norms.k_weight[plain]
+    cast = lambda v: f64(torch.tensor(v).bfloat16())   # noqa: E731
+    near, mid = 2.0 ** -20 * np.abs(x), cast(x)
+    step = cast(x + near) - cast(x - near)
+    y = oracle.rope(mid, np.asarray(pos)[:, None], r.olayer.rope_theta, r.olayer.rope_partial)
+    half = d // 2
+    pair = 2.0 ** -22 * (np.abs(mid[..., :half]) + np.abs(mid[..., half:])) + step[..., :half] + step[..., half:]
+    near = np.where(np.isin(np.arange(d), turned), np.concatenate([pair, pair], -1), step)
+    out = cast(y)
+    return out, np.maximum(cast(y + near) - out, out - cast(y - near))
+
+
+@pytest.mark.parametrize("kind,tp", [("sliding", 1), ("sliding", 8), ("global", 1), ("global", 4)])
+def test_decode_normed_against_fp64(kind, tp):
+    """Lengths within and beyond the window, page weights on global layers; a row's tolerance grows only by the columns of
+    its query that lie next to a border between two bf16 numbers."""
+    r = Rows4(kind, [45, 600, 1500, 2300], seed=36, gap=0, tp=tp, norms=Norms(kind, 9))
+    r.fill()
+    s = Step4(r, weights=kind == "global")
+    s.run()
+    status_ok()
+    q, steps = normed_turned_queries(r, s.q, s.pos)
+    scale, got, slack = r.layer.softmax_scale, f64(s.out), []
+    for b, n in enumerate(s.lens):
+        k, v = kv8.keys_values(r.olayer, *r.values(b))
+        lo = max(0, n - r.layer.window) if kind == "sliding" else 0
+        want, p, mag, peak = kv8.decode(q[b], k, v, scale, lo)
+        more = border(steps[b], k, scale)
+        assert_row(got[b], want, mag, peak, more)
+        slack += list(more[:, 0])
+        if s.weights is not None:
+            w, sums = f64(s.weights[b]), kv8.page_sums(p)
+            assert np.allclose(w[:len(sums)], sums, rtol=2e-5 + more.max(), atol=1e-9), b
+            assert (w[len(sums):] == 0).all()
+    assert np.median(slack) < 2.0 ** -9                  # half of the heads are held to the roundings alone
