@@ -463,7 +463,8 @@ g4_status g4attn_kv8_decode(const g4attn_layer* layer, const g4attn_norms* norms
  * No value is off by more than 2^E, a seventh to two sevenths of a. A block with a < 2^-77 is zeros with s = 0; when
  * x holds an infinity or NaN, every block of the vector has s = 255 and zero codes and the vector reads as NaN. The
  * value, code * 2^E, is a bf16 number. A key's bytes never depend on the batch, on the chunks its prompt came in, or
- * on later tokens, so the calls below are batch-invariant like the bf16 ones.
+ * on later tokens, so the calls below are batch-invariant like the bf16 ones. Attention sums values in fp32 before it
+ * divides by the softmax sum, as over the other caches: n values of 2^128 / n and more can overflow.
  *
  * Layout. pages holds one block per (page, KV head), 16 keys each, blocks of
  *   sliding 4368 bytes: [K' tile, 2048][V tile, 2048][scales of K', 16 x 8][of V, 16 x 8][tops of V, 16],
@@ -526,7 +527,7 @@ g4_status g4attn_kv4_decode(const g4attn_layer* layer, const g4attn_norms* norms
  * of its evictable pages leave: all but the first first_pages and the last last_pages (first_pages >= 0,
  * last_pages >= 1, first_pages + last_pages <= keep_pages). Of equal weights the lower index leaves
  * first; a NaN counts as the heaviest. No key moves: the table is closed up, in order. From then on the
- * sequence's positions run ahead of its held keys: continue it by g4attn_kv8_decode with pos alone.
+ * sequence's positions run ahead of its held keys: continue it by g4attn_kv8_decode or g4attn_kv4_decode with pos alone.
  *   out_seq_len [B]             seq_len - 16 per evicted page
  *   out_table, out_weights [B][max_pages]  the kept pages and their weights, then -1 and 0
  *   freed [B][max_pages], n_freed [B]      the evicted physical pages in their order, then -1

@@ -572,7 +572,7 @@ def g4attn_kv4_page_bytes(layer) -> int:
 
 
 def g4attn_kv4_append(layer, norms, k, v, q_start, q_len, ctx_start, cache: g4attn_cache4, page_table, stream=None):
-    """g4attn_kv_append_normed into an 4-bit cache; norms may be None. Rows are turned by their held index: a
+    """g4attn_kv_append_normed into a 4-bit cache; norms may be None. Rows are turned by their held index: a
     sequence that lost pages is continued by g4attn_kv4_decode with pos instead."""
     bf, i32, _, _, _ = _names or _torch_names()
     T, B, width = k.shape[0], q_start.shape[0], page_table.shape[-1]

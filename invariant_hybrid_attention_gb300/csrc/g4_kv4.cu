@@ -112,8 +112,9 @@ struct AppendArgs {
 // arithmetic. Sliding: half a warp per vector, two heads at a time, K' then V. Global: a warp per head for S, then
 // 8 lanes per head for the turned columns of up to four heads at once.
 // The 4 x 4096 sliding rows take 70 us with cold caches in blocks of four warps (340 MB, 4.8 TB/s, 72% of the copy rate; the
-// ALU pipe 55%, 2.9 instructions a cycle) and 2 less in blocks of one, the 2 x 8192 global ones 33 us timed by events, some
-// 6 of which an empty stretch reads too (89 MB).
+// ALU pipe 55%, 2.9 instructions a cycle) and 68 in blocks of one; the 2 x 8192 global ones 29 (89 MB, 3.0 TB/s, DRAM 30%
+// busy, 2.4 instructions a cycle, long-scoreboard stalls of 1.8 an issue: a row's loads are issued once, before its place is
+// known) and 24 with the rows in L2. A decode step's token (one row a request) adds 2.1 us to a lone step of 37 keys.
 template <bool GLOBAL, bool NORM, int MODE>
 __global__ void __launch_bounds__(kAppendWarps * 32, kAppendBlocks) kv4_append_kernel(const AppendArgs p) {
   using Blk = Kv4Block<GLOBAL>;
@@ -246,7 +247,8 @@ G4_DEV uint4 eight_bf16(uint32_t lo16, uint32_t hi16, float factor) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Bound by its loads: the 4 x 4096 sliding rows take 54 us (56 with cold caches; 340 MB, 6.1 to 6.3 TB/s). Blocks of four
+// Bound by its loads: the 4 x 4096 sliding rows take 54 us (56 with cold caches; 340 MB, 6.1 to 6.3 TB/s), the 2 x 8192
+// global ones 17 with the pages in L2 and 19 with cold caches (106 MB, 5.7 TB/s). Blocks of four
 // warps, eight an SM and two rounds of them: against blocks of eight warps, 0.5 us less for small calls, the same for large
 // ones; blocks of one warp 1 us less for the large call and 6 more for 64 single rows, many warps looking for few pages.
 constexpr int kUnpackWarps = 4, kUnpackBlocks = 8;

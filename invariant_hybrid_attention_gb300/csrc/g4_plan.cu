@@ -442,8 +442,11 @@ cudaError_t launch(const PlanArgs& p, unsigned blocks, cudaStream_t s) {
 cudaError_t launch_plan_pages(const PlanArgs& p, cudaStream_t s) {
   // Few requests: a small block, whose barriers are short, and one of them while its threads can take the rows in a few
   // turns (64 decoding requests take 3.7 us, with 16 blocks 4.1, with the large block 5.2; 300 mixed ones with 32 thousand
-  // rows 8.0, with a cluster of 8 11.2). Many: two rows or pages a thread at a time (4096 requests, 110 thousand rows: 24.2
-  // us; one takes 1.6 more, four 4.5 more).
+  // rows 8.0, with a cluster of 8 11.2). The rule looks at the rows, not at the pages that come back, which the lengths
+  // alone tell: a lone block hands them out 256 at a time, so that a step of 64 in which four requests of 32768 keys end
+  // takes 26 us, one in which all do 347 (of 300 requests, by the cluster, one of 131072 keys ends in 6.7). Many requests:
+  // two rows or pages a thread at a time (4096 requests, 110 thousand rows: 24.2 us; one takes 1.6 more, four 4.5 more),
+  // held to 64 registers with 168 bytes spilled.
   if (p.B <= 256) return launch<1, 256, 1>(p, p.T <= 1024 ? 1 : 16, s);
   if (p.B <= 1024) return launch<1, 1024, 1>(p, 16, s);
   return launch<kPlanRequests / 1024, 1024, 2>(p, 16, s);

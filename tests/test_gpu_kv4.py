@@ -862,3 +862,23 @@ def test_decode_normed_against_fp64(kind, tp):
             assert np.allclose(w[:len(sums)], sums, rtol=2e-5 + more.max(), atol=1e-9), b
             assert (w[len(sums):] == 0).all()
     assert np.median(slack) < 2.0 ** -9                  # half of the heads are held to the roundings alone
+
+
+@pytest.mark.parametrize("lens", [[300, 40], [2300, 40, 1025]])
+@pytest.mark.parametrize("kind", ["sliding", "global"])
+def test_decode_into_its_queries(kind, lens):
+    """out is q: the bits of a call with an output of its own, with one chunk and with several."""
+    r = Rows4(kind, lens, seed=37, gap=0, norms=Norms(kind, 6))
+    r.fill()
+    s = Step4(r, weights=kind == "global")
+    s.run()
+    status_ok()
+    both, weights = s.q.clone(), None if s.weights is None else torch.zeros_like(s.weights)
+    g4.g4attn_kv4_decode(r.layer, r.norms.arg, both, None, None, i32(s.lens), r.cache.desc, r.table, both, s.ws,
+                         page_weights=weights)
+    status_ok()
+    assert torch.equal(both, s.out) and (weights is None or torch.equal(weights, s.weights))
+    both = s.q.clone()
+    g4.g4attn_kv4_decode(r.layer, r.norms.arg, both, None, None, i32(s.lens), r.cache.desc, r.table, both, s.ws)
+    status_ok()
+    assert torch.equal(both, s.out)
